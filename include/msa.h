@@ -455,6 +455,105 @@ msa_status msa_encode_hidden(const void* H, int64_t n_tok, int32_t D, const void
                              void* Kbar_r, int64_t* doc_chunk_off, int64_t n_chunks, void* ws,
                              size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * The paged local context: sparse generation for a batch of requests of different lengths that
+ * come and go. Each request keeps its fixed routed memory and a local context as above
+ *   [news.neo-ai.one article, "推論パイプライン"; ruixiangma.github.io blog, "三阶段推理流程"];
+ * the local contexts share one pool of pages per layer, K_pages, V_pages
+ * [n_pages, page_size, h_kv, d] (a library service; the pages describing MSA have no
+ * counterpart). Row p of request r lies in page block_table[r, p / page_size] at row
+ * p % page_size ("slot" = page * page_size + p % page_size); keys are stored rotated at
+ * pos0 + p. A step is msa_page_plan once, then per layer msa_paged_append of the step's new
+ * rows and msa_paged_attend of their queries. New rows lie packed, request after request:
+ * row_start[r] .. row_start[r + 1] are request r's. All lengths, counts and tables are int32 in
+ * device memory, so a captured step replays with the current ones; rows behind the last
+ * request's (padding) are neither read nor written.
+ * Limits: page_size a power of two from 16 to 2^20, n_req <= 4096, the pool and a request up to
+ * 2^31 - 1 rows, h_kv <= 1024.
+ */
+
+/* msa_page_plan - block tables and slot maps of a step from the requests' lengths.
+ *
+ * target_len [n_req] length wanted of each request; len_in [n_req] length it has. A longer
+ *            target appends target - len rows; a shorter one cuts the request off there (0 ends
+ *            it). Lengths are 0 .. max_pages * page_size.
+ * block_table [n_req, max_pages] in/out: the pages of request r in its first
+ *            ceil(len / page_size) columns; entries past those are never read, and past the
+ *            new ones never written.
+ * free_list  [n_pages] in/out, n_free_in [1]: stack of the pages nobody holds (its first n_free
+ *            entries, top last). Pages given up by requests that shrink go on the stack first
+ *            (requests ascending, columns ascending); then pages needed are popped (requests
+ *            ascending, columns ascending) and entered in the table. Entries at or past the new
+ *            count are not written.
+ * len_out [n_req], n_free_out [1] the new lengths (= targets) and count; either may be the
+ *            array read (len_in, n_free_in). No other output may overlap an input.
+ * row_start  [n_req + 1] output: packed rows of the requests' new tokens.
+ * slot_map, row_pos [max_rows] outputs: each new row's slot and its row index in its request;
+ *            -1 behind the last new row.
+ * On a device-side error nothing is planned: the table and stack stay, len_out = len_in,
+ * n_free_out = n_free_in, row_start = 0, slot_map = row_pos = -1, and the status word of ws
+ * (msa_workspace_status) is 3 (a length or count out of range) or 2 (more pages needed than
+ * free, or more new rows than max_rows). A page id outside the pool found in the table or the
+ * stack gives its rows slot -1 and status 3. ws: msa_page_plan_workspace(...) bytes, 256-byte
+ * aligned; its status word is started by this call.
+ */
+size_t msa_page_plan_workspace(int32_t n_req, int32_t max_rows);
+msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
+                         const int32_t* n_free_in, int32_t n_req, int32_t page_size,
+                         int32_t max_pages, int32_t n_pages, int32_t max_rows,
+                         int32_t* block_table, int32_t* free_list, int32_t* len_out,
+                         int32_t* n_free_out, int32_t* row_start, int32_t* slot_map,
+                         int32_t* row_pos, void* ws, size_t ws_bytes, void* stream);
+
+/* msa_paged_append - K_pages[slot_map[i]] <- K_new[i] rotated at position pos0 + row_pos[i]
+ * (rope_base <= 0: as given), V_pages[slot_map[i]] <- V_new[i], for the n_rows rows of a step
+ * (K before RoPE, like K_loc); rows with a negative slot are skipped. K_new, V_new: n_rows rows
+ * of [h_kv, d], k_stride / v_stride elements apart (for slices of a fused projection; multiples
+ * of 16 bytes). Slots are distinct (of rows with one slot, any may stay). A slot past the pool
+ * is skipped and recorded in the status word of ws (>= 256 bytes, 256-byte aligned), which this
+ * call only ever sets: give it the plan's workspace, which msa_page_plan starts every step, or
+ * one that the caller zeroes. */
+msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
+                            const int32_t* slot_map, const int32_t* row_pos, const void* K_new,
+                            const void* V_new, int64_t k_stride, int64_t v_stride,
+                            int32_t n_rows, int32_t h_kv, int32_t d, int32_t dtype, int32_t pos0,
+                            float rope_base, void* ws, size_t ws_bytes, void* stream);
+
+/* msa_paged_attend - msa_sparse_attend for ragged requests over the paged local context: from
+ * single tokens to long chunks, in one batch.
+ *
+ * Q          n_rows rows of [h_q, d], q_stride elements apart (a multiple of 16 bytes), before
+ *            RoPE; row_start [n_req + 1] as written by msa_page_plan. Rows behind
+ *            row_start[n_req] are neither read nor written in O.
+ * len        [n_req] local rows of each request, its T new ones included: token i is local row
+ *            len - T + i, at position pos0 + that row. Local rows at or past len are never
+ *            looked at (they may hold anything). A chunk longer than len has tokens before row
+ *            0: they see the memory only.
+ * ctxK, ctxV [n_req, max_ctx, h_kv, d], ctx_len [n_req] gathered memory rows, used as stored
+ *            (max_ctx = 0: none, the three may be NULL).
+ * O          [n_rows, h_q, d]: softmax over {memory rows < ctx_len[r]} U {local rows <= the
+ *            token's own} of scale * q.k (scale <= 0: 1/sqrt(d)), times V; 0 for a token that
+ *            sees nothing. fp32 accumulation and softmax; bf16 inputs enter the tensor cores
+ *            with the rotated query and the probabilities rounded to bf16.
+ * Rows of the request that a token does not see are given weight 0 exactly, but they are read
+ * with the tile they share with visible ones: their V must be finite.
+ * A request whose length, row starts or pages are out of range is recorded in the status word
+ * (3); its rows of O are unspecified or not written, other requests' are right.
+ * ws         msa_paged_attend_workspace(...) bytes, 256-byte aligned, not shared with a call
+ *            that runs at the same time. The result does not depend on its contents.
+ */
+size_t msa_paged_attend_workspace(int32_t n_rows, int32_t n_req, int32_t h_q, int32_t h_kv,
+                                  int32_t d, int32_t dtype, int32_t max_ctx, int32_t max_pages,
+                                  int32_t page_size);
+msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
+                            const int32_t* row_start, const int32_t* len, int32_t n_req,
+                            const void* K_pages, const void* V_pages, int32_t n_pages,
+                            int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                            const void* ctxK, const void* ctxV, const int32_t* ctx_len,
+                            int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
+                            int32_t pos0, float rope_base, float scale, void* O, void* ws,
+                            size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

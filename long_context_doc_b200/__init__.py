@@ -37,7 +37,8 @@ SYMBOLS = ("msa_status_string", "msa_last_error", "msa_version", "msa_set_device
            "msa_decode_step_workspace", "msa_decode_step", "msa_encode_hidden_workspace",
            "msa_encode_hidden", "msa_sparse_attend_backward_workspace",
            "msa_sparse_attend_backward", "msa_scatter_bank_grad", "msa_aux_routing_loss_workspace",
-           "msa_aux_routing_loss")
+           "msa_aux_routing_loss", "msa_page_plan_workspace", "msa_page_plan", "msa_paged_append",
+           "msa_paged_attend_workspace", "msa_paged_attend")
 
 
 class MSAError(RuntimeError):
@@ -128,6 +129,19 @@ def _load():
     L.msa_decode_step.restype = ctypes.c_int
     L.msa_decode_step.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, i32, i32,
                                   i32, i32, i32, f32, f32, vp, vp, sz, vp]
+    L.msa_page_plan_workspace.restype = sz
+    L.msa_page_plan_workspace.argtypes = [i32, i32]
+    L.msa_page_plan.restype = ctypes.c_int
+    L.msa_page_plan.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp,
+                                vp, sz, vp]
+    L.msa_paged_append.restype = ctypes.c_int
+    L.msa_paged_append.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32,
+                                   i32, f32, vp, sz, vp]
+    L.msa_paged_attend_workspace.restype = sz
+    L.msa_paged_attend_workspace.argtypes = [i32] * 9
+    L.msa_paged_attend.restype = ctypes.c_int
+    L.msa_paged_attend.argtypes = [vp, i64, i32, i32, vp, vp, i32, vp, vp, i32, i32, vp, i32, vp,
+                                   vp, vp, i32, i32, i32, i32, i32, f32, f32, vp, vp, sz, vp]
     return L
 
 
@@ -377,6 +391,53 @@ def msa_aux_routing_loss(Q_r, Kbar_r, positive_bits, tau, loss, dQ_r, dKbar_r, w
                                     _s(stream)))
 
 
+def msa_page_plan_workspace(n_req, max_rows) -> int:
+    return int(lib.msa_page_plan_workspace(n_req, max_rows))
+
+
+def msa_page_plan(target_len, len_in, n_free_in, page_size, block_table, free_list, len_out,
+                  n_free_out, row_start, slot_map, row_pos, ws, stream=None):
+    n_req, max_pages = block_table.shape
+    _check(lib.msa_page_plan(_p(target_len), _p(len_in), _p(n_free_in), n_req, page_size,
+                             max_pages, free_list.shape[0], slot_map.shape[0], _p(block_table),
+                             _p(free_list), _p(len_out), _p(n_free_out), _p(row_start),
+                             _p(slot_map), _p(row_pos), _p(ws), ws.numel() * ws.element_size(),
+                             _s(stream)))
+
+
+def msa_paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, rope_base, ws,
+                     stream=None):
+    """K_pages, V_pages [n_pages, page_size, h_kv, d]; K_new, V_new [n_rows, h_kv, d], rows of
+    any stride."""
+    n_pages, page, h_kv, d = K_pages.shape
+    _check(lib.msa_paged_append(_p(K_pages), _p(V_pages), n_pages, page, _p(slot_map),
+                                _p(row_pos), _p(K_new), _p(V_new), K_new.stride(0),
+                                V_new.stride(0), K_new.shape[0], h_kv, d, dtype_code(K_pages),
+                                pos0, rope_base, _p(ws), ws.numel() * ws.element_size(),
+                                _s(stream)))
+
+
+def msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype, max_ctx, max_pages,
+                               page_size) -> int:
+    return int(lib.msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype, max_ctx,
+                                              max_pages, page_size))
+
+
+def msa_paged_attend(Q, row_start, length, K_pages, V_pages, block_table, ctxK, ctxV, ctx_len,
+                     pos0, rope_base, scale, O, ws, stream=None):
+    """Q [n_rows, h_q, d], rows of any stride; O [n_rows, h_q, d]; ctxK, ctxV, ctx_len may be
+    None (no routed memory)."""
+    n_rows, h_q, d = Q.shape
+    n_pages, page, h_kv, _ = K_pages.shape
+    n_req, max_pages = block_table.shape
+    _check(lib.msa_paged_attend(_p(Q), Q.stride(0), n_rows, h_q, _p(row_start), _p(length), n_req,
+                                _p(K_pages), _p(V_pages), n_pages, page, _p(block_table),
+                                max_pages, _p(ctxK), _p(ctxV), _p(ctx_len),
+                                0 if ctxK is None else ctxK.shape[1], h_kv, d, dtype_code(Q),
+                                pos0, rope_base, scale, _p(O), _p(ws),
+                                ws.numel() * ws.element_size(), _s(stream)))
+
+
 # ----------------------------------------------------------------------------- helpers
 def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -581,3 +642,215 @@ def aux_routing_loss(Q_r, Kbar_r, positive_bits, tau: float = 0.1, stream=None):
     ws = _ws(int(lib.msa_aux_routing_loss_workspace(B, n_chunks)), dev)
     msa_aux_routing_loss(Q_r, Kbar_r, positive_bits, tau, loss, dQ, dK, ws, stream)
     return loss, dQ, dK
+
+
+# ----------------------------------------------------------------------------- paged context
+def _same(what: str, ref: torch.Tensor, **tensors):
+    """Checks what the pointers handed to the library cannot show: the device, the type of
+    index arrays and the layout. ``None`` entries are skipped."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != ref.device:
+            raise MSAError(1, f"{what}: {name} is on {t.device}, not {ref.device}")
+        if not t.is_contiguous():
+            raise MSAError(1, f"{what}: {name} is not contiguous")
+
+
+def _int32(what: str, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != torch.int32:
+            raise MSAError(1, f"{what}: {name} is {t.dtype}, not int32")
+
+
+def _packed(what: str, name: str, t: torch.Tensor, rows: int, heads: int, d: int, ref):
+    """t: [rows, heads, d] on ref's device with ref's type, each row dense."""
+    if tuple(t.shape) != (rows, heads, d):
+        raise MSAError(1, f"{what}: {name} is {tuple(t.shape)}, not {(rows, heads, d)}")
+    if t.dtype != ref.dtype or t.device != ref.device:
+        raise MSAError(1, f"{what}: {name} is {t.dtype} on {t.device}, not {ref.dtype} on "
+                          f"{ref.device}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise MSAError(1, f"{what}: the rows of {name} are not dense")
+
+
+def _need(what: str, ok: bool, text: str):
+    if not ok:
+        raise MSAError(1, f"{what}: {text}")
+
+
+def page_plan_buffers(n_req: int, max_rows: int, device="cuda") -> dict:
+    """Output tensors of ``page_plan`` (for its ``out``)."""
+    def i32(n):
+        return torch.zeros(n, dtype=torch.int32, device=device)
+    return dict(length=i32(n_req), n_free=i32(1), row_start=i32(n_req + 1),
+                slot_map=i32(max_rows), row_pos=i32(max_rows))
+
+
+def page_plan(target, length, n_free, block_table, free_list, page_size: int, max_rows: int,
+              out: Optional[dict] = None, ws=None, stream=None) -> dict:
+    """Block tables and slot maps of a step, from the requests' lengths: ``block_table``
+    [n_req, max_pages] and ``free_list`` [n_pages] are updated in place; returns dict(length,
+    n_free, row_start, slot_map, row_pos). ``out`` gives these tensors (its length and n_free
+    may be the arguments themselves); device-side errors are in the status word of ``ws``."""
+    n_req = block_table.shape[0]
+    if out is None:
+        out = page_plan_buffers(n_req, max_rows, block_table.device)
+    if ws is None:
+        ws = _ws(msa_page_plan_workspace(n_req, max_rows), block_table.device)
+    arrays = dict(target=target, length=length, n_free=n_free, free_list=free_list, **{
+        "out " + k: v for k, v in out.items()})
+    _int32("page_plan", block_table=block_table, **arrays)
+    _same("page_plan", block_table, block_table=block_table, ws=ws, **arrays)
+    sizes = dict(target=n_req, length=n_req, n_free=1, free_list=free_list.shape[0],
+                 **{"out length": n_req, "out n_free": 1, "out row_start": n_req + 1,
+                    "out slot_map": max_rows, "out row_pos": max_rows})
+    for name, t in arrays.items():
+        _need("page_plan", t.numel() == sizes[name],
+              f"{name} has {t.numel()} elements, not {sizes[name]}")
+    with _on(block_table):
+        msa_page_plan(target, length, n_free, page_size, block_table, free_list, out["length"],
+                      out["n_free"], out["row_start"], out["slot_map"], out["row_pos"], ws, stream)
+    return out
+
+
+def _pool(what: str, K_pages, V_pages):
+    _need(what, K_pages.dim() == 4 and K_pages.shape == V_pages.shape and
+          K_pages.dtype == V_pages.dtype, "K_pages and V_pages are [n_pages, page_size, h_kv, d]")
+    _same(what, K_pages, K_pages=K_pages, V_pages=V_pages)
+
+
+class _on:
+    """Makes a tensor's device current for a launch (nothing to do when it is)."""
+    __slots__ = ("index", "back")
+
+    def __init__(self, t: torch.Tensor):
+        self.index = t.device.index
+
+    def __enter__(self):
+        self.back = None
+        if self.index is not None and torch.cuda.current_device() != self.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, rope_base: float,
+                 ws=None, stream=None):
+    """Writes a step's new rows [n_rows, h_kv, d] (rows of any stride) into their pages, keys
+    rotated at pos0 + row_pos. Returns the workspace, whose status word a bad slot sets; pass
+    the plan's as ``ws`` to read one status a step."""
+    _pool("paged_append", K_pages, V_pages)
+    h_kv, d = K_pages.shape[2:]
+    n_rows = K_new.shape[0]
+    _packed("paged_append", "K_new", K_new, n_rows, h_kv, d, K_pages)
+    _packed("paged_append", "V_new", V_new, n_rows, h_kv, d, K_pages)
+    _int32("paged_append", slot_map=slot_map, row_pos=row_pos)
+    _need("paged_append", slot_map.numel() >= n_rows and row_pos.numel() >= n_rows,
+          f"slot_map and row_pos cover {min(slot_map.numel(), row_pos.numel())} of {n_rows} rows")
+    if ws is None:
+        ws = torch.zeros(256, dtype=torch.uint8, device=K_pages.device)
+    _same("paged_append", K_pages, slot_map=slot_map, row_pos=row_pos, ws=ws)
+    with _on(K_pages):
+        msa_paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, rope_base, ws,
+                         stream)
+    return ws
+
+
+def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
+                 rope_base: float, ctxK=None, ctxV=None, ctx_len=None, scale: float = 0.0, O=None,
+                 ws=None, stream=None):
+    """Attention of every request's new tokens Q [n_rows, h_q, d] (packed by ``row_start``, rows
+    of any stride) over [routed memory ; paged local context of ``length`` rows]; returns O
+    [n_rows, h_q, d] (rows behind the last request's as they were)."""
+    _pool("paged_attend", K_pages, V_pages)
+    n_rows, h_q, d = Q.shape
+    n_pages, page, h_kv, _ = K_pages.shape
+    n_req, max_pages = block_table.shape
+    _packed("paged_attend", "Q", Q, n_rows, h_q, K_pages.shape[3], K_pages)
+    _int32("paged_attend", row_start=row_start, length=length, block_table=block_table,
+           ctx_len=ctx_len)
+    _need("paged_attend", row_start.numel() == n_req + 1 and length.numel() == n_req,
+          f"row_start and length do not fit {n_req} requests")
+    max_ctx = 0
+    if ctxK is not None:
+        max_ctx = ctxK.shape[1]
+        _need("paged_attend", ctxV is not None and ctx_len is not None and
+              ctx_len.numel() == n_req and ctxK.shape == ctxV.shape and
+              tuple(ctxK.shape) == (n_req, max_ctx, h_kv, d) and ctxK.dtype == Q.dtype and
+              ctxV.dtype == Q.dtype, "the memory is ctxK, ctxV [n_req, max_ctx, h_kv, d] and "
+                                     "ctx_len [n_req]")
+    if O is None:
+        O = torch.empty((n_rows, h_q, d), dtype=Q.dtype, device=Q.device)
+    _need("paged_attend", O.shape == Q.shape and O.dtype == Q.dtype, "O is not like Q")
+    with _on(K_pages):
+        if ws is None:
+            ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q),
+                                                max_ctx, max_pages, page), Q.device)
+        _same("paged_attend", K_pages, row_start=row_start, length=length, O=O, ws=ws,
+              block_table=block_table, ctxK=ctxK, ctxV=ctxV, ctx_len=ctx_len)
+        msa_paged_attend(Q, row_start, length, K_pages, V_pages, block_table, ctxK, ctxV, ctx_len,
+                         pos0, rope_base, scale, O, ws, stream)
+    return O
+
+
+class PagedCache:
+    """Paged local K/V of sparse generation for up to ``n_req`` requests of different lengths:
+    one pool of ``n_pages`` pages per layer (K, V [n_layers, n_pages, page_size, h_kv, d]), one
+    block table, one stack of free pages and one array of lengths for all layers, in device
+    memory. A step is ``plan`` once, then ``append`` and ``attend`` of each layer; the calls
+    read the lengths on the device, so a captured step replays as the requests grow, end
+    (target 0) and begin. Keys are stored rotated at pos0 + row (RoPE base ``rope_base``)."""
+
+    def __init__(self, n_req: int, n_pages: int, page_size: int, max_pages: int, max_rows: int,
+                 h_kv: int, d: int, n_layers: int = 1, pos0: int = 0, rope_base: float = 0.0,
+                 dtype=torch.bfloat16, device="cuda"):
+        self.pos0, self.rope_base, self.page_size = int(pos0), float(rope_base), int(page_size)
+        self.max_rows = int(max_rows)
+        self.K = torch.empty((n_layers, n_pages, page_size, h_kv, d), dtype=dtype, device=device)
+        self.V = torch.empty_like(self.K)
+        self.block_table = torch.full((n_req, max_pages), -1, dtype=torch.int32, device=device)
+        # the top of the stack is its last entry: pages are given out in ascending order
+        self.free_list = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.out = page_plan_buffers(n_req, max_rows, device)
+        self.out["n_free"].fill_(n_pages)
+        self.length, self.n_free = self.out["length"], self.out["n_free"]
+        self.ws = torch.zeros(max(256, msa_page_plan_workspace(n_req, max_rows)),
+                              dtype=torch.uint8, device=device)
+        self._attend_ws = None
+
+    def plan(self, target, stream=None) -> dict:
+        """Moves every request to its target length (int32 [n_req], device memory) and returns
+        the step's dict(length, n_free, row_start, slot_map, row_pos)."""
+        return page_plan(target, self.length, self.n_free, self.block_table, self.free_list,
+                         self.page_size, self.max_rows, out=self.out, ws=self.ws, stream=stream)
+
+    def append(self, layer: int, K_new, V_new, stream=None):
+        """Writes the planned rows (K_new, V_new [rows, h_kv, d], padding allowed) of a layer."""
+        paged_append(self.K[layer], self.V[layer], self.out["slot_map"], self.out["row_pos"],
+                     K_new, V_new, self.pos0, self.rope_base, ws=self.ws, stream=stream)
+
+    def attend(self, layer: int, Q, ctxK=None, ctxV=None, ctx_len=None, scale: float = 0.0, O=None,
+               ws=None, stream=None):
+        """Attention of the planned rows' queries Q [rows, h_q, d] of a layer. Without ``ws`` the
+        cache's own workspace serves: calls that overlap on the GPU need one each."""
+        if ws is None:
+            n_req, max_pages = self.block_table.shape
+            need = msa_paged_attend_workspace(Q.shape[0], n_req, Q.shape[1], self.K.shape[3],
+                                              self.K.shape[4], dtype_code(self.K),
+                                              0 if ctxK is None else ctxK.shape[1], max_pages,
+                                              self.page_size)
+            if self._attend_ws is None or self._attend_ws.numel() < need:
+                self._attend_ws = _ws(need, self.K.device)
+            ws = self._attend_ws
+        return paged_attend(Q, self.out["row_start"], self.length, self.K[layer], self.V[layer],
+                            self.block_table, self.pos0, self.rope_base, ctxK, ctxV, ctx_len,
+                            scale, O, ws, stream)
+
+    def status(self, stream=None) -> int:
+        """Status word of the last plan and the appends since (0 = no device error); synchronises
+        the stream."""
+        return msa_workspace_status(self.ws, stream)

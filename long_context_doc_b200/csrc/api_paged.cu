@@ -1,0 +1,252 @@
+// api_paged.cu - the extern "C" boundary of the paged local context (declared in
+// include/msa.h): argument validation, workspace sizing and launches, as api.cu.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/msa.h"
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace {
+
+msa_status fail(msa_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+msa_status fail(msa_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  msa::set_last_error(buf);
+  return s;
+}
+
+msa_status done(cudaError_t e, const char* what) {
+  if (e != cudaSuccess)
+    return fail(MSA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+  msa::set_last_error("");
+  return MSA_OK;
+}
+
+#define REQUIRE(cond, status, ...) \
+  do {                             \
+    if (!(cond)) return fail(status, __VA_ARGS__); \
+  } while (0)
+
+constexpr size_t kHeader = 256;
+constexpr int32_t kMinPage = 16, kMaxHeads = 1024;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t esize(int dtype) { return dtype == MSA_BF16 ? 2 : 4; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 148;
+  return n;
+}
+
+int log2i(int32_t x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+msa_status check_pool(int32_t page_size, int32_t n_pages, int32_t max_pages, int32_t n_req) {
+  REQUIRE(page_size >= kMinPage && page_size <= (1 << 20) && (page_size & (page_size - 1)) == 0,
+          MSA_ERR_UNSUPPORTED, "page size %d (a power of two from %d to 2^20)", page_size, kMinPage);
+  REQUIRE(n_pages >= 1 && (int64_t)n_pages * page_size < (1ll << 31), MSA_ERR_INVALID_ARG,
+          "n_pages %d (the pool holds 1 to 2^31 - 1 rows)", n_pages);
+  REQUIRE(max_pages >= 1 && (int64_t)max_pages * page_size < (1ll << 31), MSA_ERR_INVALID_ARG,
+          "max_pages %d (a request holds up to 2^31 - 1 rows)", max_pages);
+  REQUIRE(n_req >= 0, MSA_ERR_INVALID_ARG, "n_req %d", n_req);
+  REQUIRE(n_req <= msa::kPagedMaxReq, MSA_ERR_UNSUPPORTED, "n_req %d (up to %d)", n_req,
+          msa::kPagedMaxReq);
+  return MSA_OK;
+}
+
+msa_status check_heads(int32_t h_kv, int32_t d, int32_t dtype) {
+  REQUIRE(dtype == MSA_FP32 || dtype == MSA_BF16, MSA_ERR_UNSUPPORTED, "dtype %d", dtype);
+  REQUIRE(d == 64 || d == 128, MSA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", d);
+  REQUIRE(h_kv >= 1, MSA_ERR_INVALID_ARG, "h_kv %d", h_kv);
+  REQUIRE(h_kv <= kMaxHeads, MSA_ERR_UNSUPPORTED, "h_kv %d (up to %d)", h_kv, kMaxHeads);
+  return MSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t msa_page_plan_workspace(int32_t n_req, int32_t max_rows) {
+  (void)n_req;
+  (void)max_rows;
+  return kHeader;
+}
+
+msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
+                         const int32_t* n_free_in, int32_t n_req, int32_t page_size,
+                         int32_t max_pages, int32_t n_pages, int32_t max_rows,
+                         int32_t* block_table, int32_t* free_list, int32_t* len_out,
+                         int32_t* n_free_out, int32_t* row_start, int32_t* slot_map,
+                         int32_t* row_pos, void* ws, size_t ws_bytes, void* stream) {
+  msa_status s = check_pool(page_size, n_pages, max_pages, n_req);
+  if (s != MSA_OK) return s;
+  REQUIRE(max_rows >= 0, MSA_ERR_INVALID_ARG, "max_rows %d", max_rows);
+  REQUIRE(ws != nullptr && ws_bytes >= kHeader && aligned(ws, 256), MSA_ERR_WORKSPACE,
+          "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, kHeader);
+  REQUIRE(n_free_in && n_free_out && row_start && free_list, MSA_ERR_INVALID_ARG, "null pointer");
+  REQUIRE(n_req == 0 || (target_len && len_in && block_table && len_out), MSA_ERR_INVALID_ARG,
+          "null pointer");
+  REQUIRE(max_rows == 0 || (slot_map && row_pos), MSA_ERR_INVALID_ARG, "null row map");
+  msa::PagePlanParams p{};
+  p.target = target_len;
+  p.len_in = len_in;
+  p.nfree_in = n_free_in;
+  p.table = block_table;
+  p.free_list = free_list;
+  p.len_out = len_out;
+  p.nfree_out = n_free_out;
+  p.row_start = row_start;
+  p.slot_map = slot_map;
+  p.row_pos = row_pos;
+  p.n_req = n_req;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.page_shift = log2i(page_size);
+  p.max_rows = max_rows;
+  p.vec = aligned(slot_map, 16) && aligned(row_pos, 16);
+  p.err = static_cast<int*>(ws);
+  return done(msa::launch_page_plan(p, (cudaStream_t)stream), "msa_page_plan launch");
+}
+
+msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
+                            const int32_t* slot_map, const int32_t* row_pos, const void* K_new,
+                            const void* V_new, int64_t k_stride, int64_t v_stride,
+                            int32_t n_rows, int32_t h_kv, int32_t d, int32_t dtype, int32_t pos0,
+                            float rope_base, void* ws, size_t ws_bytes, void* stream) {
+  msa_status s = check_heads(h_kv, d, dtype);
+  if (s == MSA_OK) s = check_pool(page_size, n_pages, 1, 0);
+  if (s != MSA_OK) return s;
+  REQUIRE(n_rows >= 0 && pos0 >= 0, MSA_ERR_INVALID_ARG, "bad sizes (n_rows=%d pos0=%d)", n_rows,
+          pos0);
+  REQUIRE(ws != nullptr && ws_bytes >= kHeader && aligned(ws, 256), MSA_ERR_WORKSPACE,
+          "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, kHeader);
+  if (n_rows == 0) return done(cudaSuccess, "");
+  const int64_t row = (int64_t)h_kv * d, per16 = 16 / (int64_t)esize(dtype);
+  REQUIRE(slot_map && row_pos && K_new && V_new && K_pages && V_pages, MSA_ERR_INVALID_ARG,
+          "null tensor");
+  REQUIRE(k_stride >= row && v_stride >= row && k_stride % per16 == 0 && v_stride % per16 == 0,
+          MSA_ERR_INVALID_ARG, "row strides %lld, %lld (at least h_kv * d, multiples of 16 bytes)",
+          (long long)k_stride, (long long)v_stride);
+  REQUIRE(aligned(K_new, 16) && aligned(V_new, 16) && aligned(K_pages, 16) && aligned(V_pages, 16),
+          MSA_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  msa::PagedAppendParams p{};
+  p.K_new = K_new;
+  p.V_new = V_new;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slot_map = slot_map;
+  p.row_pos = row_pos;
+  p.K_pages = K_pages;
+  p.V_pages = V_pages;
+  p.n_slots = (int64_t)n_pages * page_size;
+  p.n_rows = n_rows;
+  p.h_kv = h_kv;
+  p.rope = rope_base > 0.f ? 1 : 0;
+  p.pos0 = pos0;
+  msa::rope_turns(p.rope ? (double)rope_base : 0.0, d, p.rope_turns);
+  p.err = static_cast<int*>(ws);
+  return done(msa::launch_paged_append(p, dtype, d, sm_count(), (cudaStream_t)stream),
+              "msa_paged_append launch");
+}
+
+size_t msa_paged_attend_workspace(int32_t n_rows, int32_t n_req, int32_t h_q, int32_t h_kv,
+                                  int32_t d, int32_t dtype, int32_t max_ctx, int32_t max_pages,
+                                  int32_t page_size) {
+  if (n_rows < 1 || n_req < 1 || h_kv < 1 || h_kv > kMaxHeads || h_q < h_kv || d < 1)
+    return kHeader;
+  (void)dtype;
+  (void)max_ctx;
+  (void)max_pages;
+  (void)page_size;
+  const msa::PagedPlan pl = msa::paged_attend_plan(n_req, h_kv, d, dtype, sm_count());
+  return kHeader + pl.err_bytes + pl.tail_bytes + pl.ml_bytes + pl.o_bytes;
+}
+
+msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
+                            const int32_t* row_start, const int32_t* len, int32_t n_req,
+                            const void* K_pages, const void* V_pages, int32_t n_pages,
+                            int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                            const void* ctxK, const void* ctxV, const int32_t* ctx_len,
+                            int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
+                            int32_t pos0, float rope_base, float scale, void* O, void* ws,
+                            size_t ws_bytes, void* stream) {
+  msa_status s = check_heads(h_kv, d, dtype);
+  if (s == MSA_OK) s = check_pool(page_size, n_pages, max_pages, n_req);
+  if (s != MSA_OK) return s;
+  REQUIRE(h_q >= h_kv && h_q % h_kv == 0, MSA_ERR_INVALID_ARG, "h_q %d not a multiple of h_kv %d",
+          h_q, h_kv);
+  REQUIRE(n_rows >= 0 && (int64_t)n_rows * h_q < (1ll << 31) && max_ctx >= 0 && pos0 >= 0,
+          MSA_ERR_INVALID_ARG, "bad sizes (n_rows=%d h_q=%d max_ctx=%d pos0=%d)", n_rows, h_q,
+          max_ctx, pos0);
+  REQUIRE(scale == scale && std::fabs(scale) <= 3.0e38f, MSA_ERR_INVALID_ARG,
+          "scale is not finite");
+  const size_t need = msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype, max_ctx,
+                                                 max_pages, page_size);
+  REQUIRE(ws != nullptr && ws_bytes >= need && aligned(ws, 256), MSA_ERR_WORKSPACE,
+          "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, need);
+  const int64_t per16 = 16 / (int64_t)esize(dtype);
+  if (n_rows > 0 && n_req > 0) {
+    REQUIRE(Q && row_start && len && K_pages && V_pages && block_table && O, MSA_ERR_INVALID_ARG,
+            "null tensor");
+    REQUIRE(max_ctx == 0 || (ctxK && ctxV && ctx_len), MSA_ERR_INVALID_ARG, "null context");
+    REQUIRE(q_stride >= (int64_t)h_q * d && q_stride % per16 == 0, MSA_ERR_INVALID_ARG,
+            "Q row stride %lld (at least h_q * d, a multiple of 16 bytes)", (long long)q_stride);
+    REQUIRE(aligned(Q, 16) && aligned(K_pages, 16) && aligned(V_pages, 16) && aligned(O, 16) &&
+                (max_ctx == 0 || (aligned(ctxK, 16) && aligned(ctxV, 16))),
+            MSA_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  if (n_rows == 0 || n_req == 0)  // nothing to do but to start the status word
+    return done(cudaMemsetAsync(ws, 0, sizeof(int32_t), st), "msa_paged_attend");
+  msa::PagedAttendParams p{};
+  p.Q = Q;
+  p.q_stride = q_stride;
+  p.row_start = row_start;
+  p.len = len;
+  p.n_rows = n_rows;
+  p.n_req = n_req;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.K_pages = K_pages;
+  p.V_pages = V_pages;
+  p.n_pages = n_pages;
+  p.page_shift = log2i(page_size);
+  p.table = block_table;
+  p.max_pages = max_pages;
+  p.cK = ctxK;
+  p.cV = ctxV;
+  p.ctx_len = max_ctx > 0 ? ctx_len : nullptr;
+  p.max_ctx = max_ctx;
+  p.rope = rope_base > 0.f ? 1 : 0;
+  p.pos0 = pos0;
+  msa::rope_turns(p.rope ? (double)rope_base : 0.0, d, p.rope_turns);
+  p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
+  p.O = O;
+  const msa::PagedPlan pl = msa::paged_attend_plan(n_req, h_kv, d, dtype, sm_count());
+  unsigned char* w8 = static_cast<unsigned char*>(ws);
+  p.err = reinterpret_cast<int*>(w8);
+  w8 += kHeader;
+  p.err_cta = reinterpret_cast<int*>(w8);
+  w8 += pl.err_bytes;
+  p.tail = reinterpret_cast<int4*>(w8);
+  w8 += pl.tail_bytes;
+  p.part_ml = reinterpret_cast<float*>(w8);
+  w8 += pl.ml_bytes;
+  p.part_o = reinterpret_cast<float*>(w8);
+  return done(msa::launch_paged_attend(p, pl, dtype, d, st), "msa_paged_attend launch");
+}
+
+}  // extern "C"

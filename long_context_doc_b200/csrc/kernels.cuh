@@ -325,4 +325,71 @@ cudaError_t launch_aux_routing_loss(const void* Q_r, int B, int T, int h_qr, con
                                     float* dKbar_r, unsigned char* scratch, int sms,
                                     cudaStream_t st);
 
+// ---- paged.cu: the paged local context (block tables, slot maps, append)
+constexpr int kPagedMaxReq = 4096;  // requests of one call (their prefix sums fit shared memory)
+struct PagePlanParams {
+  const int32_t* target;   // [n_req] lengths wanted
+  const int32_t* len_in;   // [n_req] lengths held
+  const int32_t* nfree_in; // [1]
+  int32_t* table;          // [n_req, max_pages]
+  int32_t* free_list;      // [n_pages], the first n_free valid
+  int32_t* len_out;        // [n_req], may be len_in
+  int32_t* nfree_out;      // [1], may be nfree_in
+  int32_t* row_start;      // [n_req + 1]
+  int32_t* slot_map;       // [max_rows]
+  int32_t* row_pos;        // [max_rows]
+  int n_req, max_pages, n_pages, page_shift, max_rows;
+  int vec;                 // slot_map and row_pos 16-byte aligned
+  int* err;
+};
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t st);
+struct PagedAppendParams {
+  const void* K_new;       // [n_rows] rows of h_kv * d elements, `stride` elements apart
+  const void* V_new;
+  int64_t k_stride, v_stride;
+  const int32_t* slot_map; // [n_rows]
+  const int32_t* row_pos;  // [n_rows]
+  void* K_pages;           // [n_slots, h_kv, d]
+  void* V_pages;
+  int64_t n_slots;
+  int n_rows, h_kv, rope, pos0;
+  unsigned long long rope_turns[64];
+  int* err;
+};
+cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
+                                cudaStream_t st);
+
+// ---- paged_attend.cu: attention of ragged requests over [routed memory ; paged local context]
+struct PagedAttendParams {
+  const void* Q;            // [n_rows] rows of h_q * d elements, q_stride elements apart
+  int64_t q_stride;
+  const int32_t* row_start; // [n_req + 1]
+  const int32_t* len;       // [n_req]
+  int n_rows, n_req, h_q, h_kv;
+  const void* K_pages;      // [n_pages << page_shift, h_kv, d], keys rotated
+  const void* V_pages;
+  int n_pages, page_shift;
+  const int32_t* table;     // [n_req, max_pages]
+  int max_pages;
+  const void* cK;           // [n_req, max_ctx, h_kv, d]
+  const void* cV;
+  const int32_t* ctx_len;   // [n_req] (nullable: no memory)
+  int max_ctx, rope, pos0;
+  unsigned long long rope_turns[64];
+  float scale_log2;
+  void* O;                  // [n_rows, h_q, d]
+  int* err;                 // status word, written by the merge kernel
+  int* err_cta;             // [grid] what each CTA of the attention kernel recorded
+  int4* tail;               // [S] the item a split begins and does not end
+  float* part_ml;           // [S][2][h_kv][rows][2]
+  float* part_o;            // [S][2][h_kv][rows][d]
+};
+struct PagedPlan {
+  int grid, S;              // CTAs; ranges that the tile list is cut into (per KV head)
+  size_t err_bytes, tail_bytes, ml_bytes, o_bytes, smem;
+};
+PagedPlan paged_attend_plan(int n_req, int h_kv, int d, int dtype, int sms);
+cudaError_t launch_paged_attend(const PagedAttendParams& p, const PagedPlan& pl, int dtype, int d,
+                                cudaStream_t st);
+
 }  // namespace msa

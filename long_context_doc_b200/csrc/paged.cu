@@ -1,0 +1,316 @@
+// paged.cu - the paged, ragged local context of sparse generation: the step's block tables and
+// slot maps from the requests' lengths, and the append of the step's rows into their pages.
+//
+// Sparse generation keeps a request's local context next to its fixed routed memory
+//   [news.neo-ai.one article, "推論パイプライン"; ruixiangma.github.io blog, "三阶段推理流程"];
+// here the local contexts of many requests of different lengths share one pool of pages of
+// 2^page_shift rows. Request r holds ceil(len_r / page) pages, listed in its row of the block
+// table; pages nobody holds lie on a stack (free_list, its first n_free entries).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace msa {
+namespace pgd {
+
+namespace cg = cooperative_groups;
+
+// ------------------------------------------------------------------------------ plan
+// One cluster of one or eight CTAs. With old = len_in, tgt = target, held(x) = ceil(x / page):
+// request r gives back the pages of its table columns [held(tgt), held(old)) or needs pages for
+// the columns [held(old), held(tgt)). Three exclusive sums over the requests (new rows, needed
+// pages, returned pages) fix everything else: the stack after the returns is
+// free_list[0 .. F) followed by the returned pages in request order, and the i-th needed page
+// is the i-th from its top, so with R returns it is returned page R-1-i, or
+// free_list[F-1-(i-R)] for i >= R. Returned pages beyond the needed ones (R > P) stay on the
+// stack at F .. F+R-P. No step depends on another's writes: entries read (below F; columns
+// below held(old)) are never entries written, so one pass over the rows fills the slots and
+// the table together.
+// Every CTA computes the sums for itself (a few microseconds less than a second launch or a
+// trip through memory); the cluster barrier after them is what lets len_out be len_in and
+// nfree_out be nfree_in. Latency-bound throughout.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanCluster = 8;
+constexpr int kPlanOneCta = 4096;  // rows up to which a single CTA fills the maps
+
+struct PlanSums {
+  long long rows, need, back;
+};
+
+// inclusive block scan of three values; totals of the block in *tot
+__device__ __forceinline__ PlanSums block_scan(PlanSums v, PlanSums* warp_tot, PlanSums* tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, v.rows, o);
+    const long long b = __shfl_up_sync(0xffffffffu, v.need, o);
+    const long long c = __shfl_up_sync(0xffffffffu, v.back, o);
+    if (lane >= o) {
+      v.rows += a;
+      v.need += b;
+      v.back += c;
+    }
+  }
+  if (lane == 31) warp_tot[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    PlanSums w = warp_tot[lane];
+    const PlanSums own = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long a = __shfl_up_sync(0xffffffffu, w.rows, o);
+      const long long b = __shfl_up_sync(0xffffffffu, w.need, o);
+      const long long c = __shfl_up_sync(0xffffffffu, w.back, o);
+      if (lane >= o) {
+        w.rows += a;
+        w.need += b;
+        w.back += c;
+      }
+    }
+    if (lane == 31) *tot = w;
+    warp_tot[lane] = PlanSums{w.rows - own.rows, w.need - own.need, w.back - own.back};
+  }
+  __syncthreads();
+  const PlanSums base = warp_tot[warp];
+  const PlanSums r{v.rows + base.rows, v.need + base.need, v.back + base.back};
+  return r;
+}
+
+// last r in [0, n) with start[r] <= x (start non-decreasing, start[0] = 0): of requests
+// without entries the last one, which is the one that owns entry x
+__device__ __forceinline__ int owner(const int32_t* start, int n, int x) {
+  int lo = 0, hi = n;  // start[lo] <= x, (hi == n or start[hi] > x)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PagePlanParams p) {
+  extern __shared__ int32_t sm[];
+  const int n = p.n_req;
+  int32_t* row_s = sm;                 // [n + 1] first new row of request r
+  int32_t* need_s = sm + (n + 1);      // [n + 1] first needed page
+  int32_t* back_s = sm + 2 * (n + 1);  // [n + 1] first returned page
+  int32_t* old_s = sm + 3 * (n + 1);   // [n]
+  int32_t* tgt_s = old_s + n;          // [n]
+  __shared__ PlanSums warp_tot[32], chunk_tot;
+  __shared__ int bad_len;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
+  const int nthreads = (int)cluster.num_blocks() * kPlanThreads;
+  const int sh = p.page_shift;
+  const int pm = (1 << sh) - 1;
+  const long long cap = (long long)p.max_pages << sh;
+
+  if (tid == 0) bad_len = 0;
+  const int F = *p.nfree_in;
+  PlanSums carry{0, 0, 0};
+  __syncthreads();
+  for (int b0 = 0; b0 < n; b0 += kPlanThreads) {
+    const int r = b0 + tid;
+    PlanSums v{0, 0, 0};
+    int old = 0, tgt = 0;
+    if (r < n) {
+      old = p.len_in[r];
+      tgt = p.target[r];
+      if (old < 0 || tgt < 0 || old > cap || tgt > cap) {
+        bad_len = 1;
+        old = tgt = 0;
+      }
+      const int ho = (int)(((long long)old + pm) >> sh), ht = (int)(((long long)tgt + pm) >> sh);
+      v.rows = max(tgt - old, 0);
+      v.need = max(ht - ho, 0);
+      v.back = max(ho - ht, 0);
+    }
+    const PlanSums s = block_scan(v, warp_tot, &chunk_tot);
+    if (r < n) {  // sums past 2^31 are caught below, before they are used
+      row_s[r] = (int32_t)(carry.rows + s.rows - v.rows);
+      need_s[r] = (int32_t)(carry.need + s.need - v.need);
+      back_s[r] = (int32_t)(carry.back + s.back - v.back);
+      old_s[r] = old;
+      tgt_s[r] = tgt;
+    }
+    carry.rows += chunk_tot.rows;
+    carry.need += chunk_tot.need;
+    carry.back += chunk_tot.back;
+    __syncthreads();  // chunk_tot and warp_tot are reused
+  }
+  int code = 0;
+  if (bad_len || F < 0 || F > p.n_pages || F + carry.back > p.n_pages) code = kErrBadIndex;
+  else if (carry.need > F + carry.back || carry.rows > p.max_rows) code = kErrCtxOverflow;
+  const int rows = code ? 0 : (int)carry.rows;
+  const int P = code ? 0 : (int)carry.need, R = code ? 0 : (int)carry.back;
+  if (tid == 0) {
+    row_s[n] = (int32_t)carry.rows;
+    need_s[n] = (int32_t)carry.need;
+    back_s[n] = (int32_t)carry.back;
+    if (rank == 0) *p.err = code;
+  }
+  // every CTA has read the lengths and the count, and the status word is started
+  __syncthreads();
+  cluster.sync();
+
+  const int gt = rank * kPlanThreads + tid;
+  for (int r = gt; r < n; r += nthreads) {
+    p.row_start[r] = code ? 0 : row_s[r];
+    p.len_out[r] = code ? p.len_in[r] : tgt_s[r];  // a refused plan keeps the lengths
+  }
+  if (gt == 0) {
+    p.row_start[n] = rows;
+    *p.nfree_out = F + R - P;
+  }
+  // column `col` of request r among its returned pages, and the i-th page off the stack
+  auto returned = [&](int q) {
+    const int r = owner(back_s, n, q);
+    const int ht = (int)(((long long)tgt_s[r] + pm) >> sh);
+    return p.table[(int64_t)r * p.max_pages + ht + (q - back_s[r])];
+  };
+  auto popped = [&](int i) { return i < R ? returned(R - 1 - i) : p.free_list[F - 1 - (i - R)]; };
+  for (int q = gt; q < R - P; q += nthreads) p.free_list[F + q] = returned(q);
+
+  // four consecutive rows a thread: one search, then a walk along the requests
+  bool bad_page = false;
+  for (int i0 = gt * 4; i0 < p.max_rows; i0 += nthreads * 4) {
+    int32_t slot[4], pos[4];
+    int r = i0 < rows ? owner(row_s, n, i0) : 0;
+    int col = -1;
+    int page = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e;
+      slot[e] = pos[e] = -1;
+      if (i >= rows) continue;
+      while (row_s[r + 1] <= i) {
+        ++r;
+        col = -1;
+      }
+      const int at = old_s[r] + (i - row_s[r]);
+      const int c = at >> sh;
+      if (c != col) {
+        col = c;
+        const int ho = (int)(((long long)old_s[r] + pm) >> sh);
+        page = c < ho ? p.table[(int64_t)r * p.max_pages + c] : popped(need_s[r] + (c - ho));
+      }
+      // the first row of a needed page enters it in the table
+      if ((at & pm) == 0) p.table[(int64_t)r * p.max_pages + c] = page;
+      pos[e] = at;
+      const bool ok = page >= 0 && page < p.n_pages;
+      bad_page |= !ok;
+      slot[e] = ok ? (page << sh) + (at & pm) : -1;
+    }
+    if (p.vec && i0 + 3 < p.max_rows) {
+      *reinterpret_cast<int4*>(p.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(p.row_pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + e < p.max_rows) {
+          p.slot_map[i0 + e] = slot[e];
+          p.row_pos[i0 + e] = pos[e];
+        }
+    }
+  }
+  if (bad_page) set_err(p.err, kErrBadIndex);
+}
+
+// ------------------------------------------------------------------------------ append
+// K_pages[slot] = R(pos0 + pos) K_new, V_pages[slot] = V_new. A warp takes a row: lane = one
+// 16-byte chunk of the lower half of a head and its partner half a head on (RoPE pairs
+// i, i + d/2), so a row's angles are computed once and serve every head. HBM-bound for many
+// rows (each row read and written once), latency for few.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendParams p) {
+  constexpr int E = 16 / sizeof(T);   // elements of a chunk
+  constexpr int HC = D / 2 / E;       // chunks of half a head
+  constexpr int HPW = 32 / HC;        // heads a warp takes at once
+  using V = Vec<T, E>;
+  using Raw = typename V::raw;
+  const int lane = threadIdx.x & 31;
+  const int c = lane % HC, h0 = lane / HC;
+  unsigned long long F[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) F[e] = p.rope_turns[c * E + e];
+  const int nw = gridDim.x * (blockDim.x >> 5);
+  for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < p.n_rows; r += nw) {
+    const int64_t slot = p.slot_map[r];
+    if (slot < 0) continue;  // a padding row
+    if (slot >= p.n_slots) {
+      if (lane == 0) set_err(p.err, kErrBadIndex);
+      continue;
+    }
+    const int64_t pos = (int64_t)p.pos0 + p.row_pos[r];
+    const T* ks = static_cast<const T*>(p.K_new) + r * p.k_stride;
+    const T* vs = static_cast<const T*>(p.V_new) + r * p.v_stride;
+    T* kd = static_cast<T*>(p.K_pages) + slot * p.h_kv * D;
+    T* vd = static_cast<T*>(p.V_pages) + slot * p.h_kv * D;
+    float2 cs[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) cs[e] = p.rope ? rot_turns(pos, F[e]) : make_float2(1.f, 0.f);
+#pragma unroll 2
+    for (int h = h0; h < p.h_kv; h += HPW) {
+      const int at = h * D + c * E;
+      const Raw ka = __ldg(reinterpret_cast<const Raw*>(ks + at));
+      const Raw kb = __ldg(reinterpret_cast<const Raw*>(ks + at + D / 2));
+      const Raw va = __ldg(reinterpret_cast<const Raw*>(vs + at));
+      const Raw vb = __ldg(reinterpret_cast<const Raw*>(vs + at + D / 2));
+      float a[E], b[E];
+      V::unpack(ka, a);
+      V::unpack(kb, b);
+      Raw oa, ob;
+      T* ta = reinterpret_cast<T*>(&oa);
+      T* tb = reinterpret_cast<T*>(&ob);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        ta[e] = Elem<T>::from_f(a[e] * cs[e].x - b[e] * cs[e].y);
+        tb[e] = Elem<T>::from_f(b[e] * cs[e].x + a[e] * cs[e].y);
+      }
+      *reinterpret_cast<Raw*>(kd + at) = oa;
+      *reinterpret_cast<Raw*>(kd + at + D / 2) = ob;
+      *reinterpret_cast<Raw*>(vd + at) = va;
+      *reinterpret_cast<Raw*>(vd + at + D / 2) = vb;
+    }
+  }
+}
+
+}  // namespace pgd
+
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t st) {
+  const int ctas = p.max_rows <= pgd::kPlanOneCta ? 1 : pgd::kPlanCluster;
+  const size_t smem = sizeof(int32_t) * (5 * (size_t)p.n_req + 3);
+  cudaError_t e = cudaFuncSetAttribute(pgd::page_plan_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(pgd::kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pgd::page_plan_kernel, p);
+}
+
+cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
+                                cudaStream_t st) {
+  if (p.n_rows == 0) return cudaSuccess;
+  const int grid = std::min((p.n_rows + 3) / 4, sms * 8);
+  if (dtype == 1)
+    d == 128 ? pgd::paged_append_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(p)
+             : pgd::paged_append_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(p);
+  else
+    d == 128 ? pgd::paged_append_kernel<float, 128><<<grid, 128, 0, st>>>(p)
+             : pgd::paged_append_kernel<float, 64><<<grid, 128, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace msa
