@@ -645,38 +645,57 @@ def aux_routing_loss(Q_r, Kbar_r, positive_bits, tau: float = 0.1, stream=None):
 
 
 # ----------------------------------------------------------------------------- paged context
-def _same(what: str, ref: torch.Tensor, **tensors):
-    """Checks what the pointers handed to the library cannot show: the device, the type of
-    index arrays and the layout. ``None`` entries are skipped."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != ref.device:
-            raise MSAError(1, f"{what}: {name} is on {t.device}, not {ref.device}")
-        if not t.is_contiguous():
-            raise MSAError(1, f"{what}: {name} is not contiguous")
-
-
-def _int32(what: str, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.int32:
-            raise MSAError(1, f"{what}: {name} is {t.dtype}, not int32")
-
-
-def _packed(what: str, name: str, t: torch.Tensor, rows: int, heads: int, d: int, ref):
-    """t: [rows, heads, d] on ref's device with ref's type, each row dense."""
-    if tuple(t.shape) != (rows, heads, d):
-        raise MSAError(1, f"{what}: {name} is {tuple(t.shape)}, not {(rows, heads, d)}")
-    if t.dtype != ref.dtype or t.device != ref.device:
-        raise MSAError(1, f"{what}: {name} is {t.dtype} on {t.device}, not {ref.dtype} on "
-                          f"{ref.device}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        raise MSAError(1, f"{what}: the rows of {name} are not dense")
-
-
+# These calls are made per layer and token, so their argument checks are one expression on the
+# way in; what it finds wrong is named by the _explain_* functions afterwards.
 def _need(what: str, ok: bool, text: str):
     if not ok:
         raise MSAError(1, f"{what}: {text}")
+
+
+def _explain_arrays(what: str, dev: int, **arrays):
+    """arrays: name -> (tensor, type or None, elements or None) of contiguous tensors."""
+    for name, (t, dtype, n) in arrays.items():
+        if t is None:
+            continue
+        _need(what, dtype is None or t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+        _need(what, t.get_device() == dev, f"{name} is on {t.device}")
+        _need(what, t.is_contiguous(), f"{name} is not contiguous")
+        _need(what, n is None or t.numel() == n, f"{name} has {t.numel()} elements, not {n}")
+
+
+def _explain_rows(what: str, name: str, t, shape, ref):
+    """t: packed rows [rows, heads, d] like ref, each row dense."""
+    _need(what, tuple(t.shape) == shape, f"{name} is {tuple(t.shape)}, not {shape}")
+    _need(what, t.dtype == ref.dtype and t.get_device() == ref.get_device(),
+          f"{name} is {t.dtype} on {t.device}, not {ref.dtype} on {ref.device}")
+    _need(what, t.stride(2) == 1 and (shape[1] == 1 or t.stride(1) == shape[2]),
+          f"the rows of {name} are not dense")
+
+
+def _explain_pool(what: str, K_pages, V_pages):
+    _need(what, K_pages.dim() == 4 and K_pages.shape == V_pages.shape,
+          "K_pages and V_pages are [n_pages, page_size, h_kv, d]")
+    _explain_arrays(what, K_pages.get_device(), K_pages=(K_pages, None, None),
+                    V_pages=(V_pages, K_pages.dtype, None))
+
+
+class _on:
+    """Makes device ``index`` current for a launch (nothing to do when it is, or for -1)."""
+    __slots__ = ("index", "back")
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.back = -1
+        if self.index >= 0:
+            self.back = torch.cuda.current_device()
+            if self.back != self.index:
+                torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back >= 0 and self.back != self.index:
+            torch.cuda.set_device(self.back)
 
 
 def page_plan_buffers(n_req: int, max_rows: int, device="cuda") -> dict:
@@ -698,44 +717,24 @@ def page_plan(target, length, n_free, block_table, free_list, page_size: int, ma
         out = page_plan_buffers(n_req, max_rows, block_table.device)
     if ws is None:
         ws = _ws(msa_page_plan_workspace(n_req, max_rows), block_table.device)
-    arrays = dict(target=target, length=length, n_free=n_free, free_list=free_list, **{
-        "out " + k: v for k, v in out.items()})
-    _int32("page_plan", block_table=block_table, **arrays)
-    _same("page_plan", block_table, block_table=block_table, ws=ws, **arrays)
-    sizes = dict(target=n_req, length=n_req, n_free=1, free_list=free_list.shape[0],
-                 **{"out length": n_req, "out n_free": 1, "out row_start": n_req + 1,
-                    "out slot_map": max_rows, "out row_pos": max_rows})
-    for name, t in arrays.items():
-        _need("page_plan", t.numel() == sizes[name],
-              f"{name} has {t.numel()} elements, not {sizes[name]}")
-    with _on(block_table):
+    dev = block_table.get_device()
+    wanted = ((target, n_req), (length, n_req), (n_free, 1), (free_list, free_list.numel()),
+              (block_table, block_table.numel()), (out["length"], n_req), (out["n_free"], 1),
+              (out["row_start"], n_req + 1), (out["slot_map"], max_rows),
+              (out["row_pos"], max_rows))
+    i32 = torch.int32
+    for t, n in wanted:
+        if (t.numel() != n or t.dtype != i32 or t.get_device() != dev or not t.is_contiguous()):
+            names = ("target", "length", "n_free", "free_list", "block_table", "out length",
+                     "out n_free", "out row_start", "out slot_map", "out row_pos")
+            _explain_arrays("page_plan", dev, **{k: (t, i32, n) for k, (t, n) in
+                                                 zip(names, wanted)})
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _explain_arrays("page_plan", dev, ws=(ws, None, None))
+    with _on(dev):
         msa_page_plan(target, length, n_free, page_size, block_table, free_list, out["length"],
                       out["n_free"], out["row_start"], out["slot_map"], out["row_pos"], ws, stream)
     return out
-
-
-def _pool(what: str, K_pages, V_pages):
-    _need(what, K_pages.dim() == 4 and K_pages.shape == V_pages.shape and
-          K_pages.dtype == V_pages.dtype, "K_pages and V_pages are [n_pages, page_size, h_kv, d]")
-    _same(what, K_pages, K_pages=K_pages, V_pages=V_pages)
-
-
-class _on:
-    """Makes a tensor's device current for a launch (nothing to do when it is)."""
-    __slots__ = ("index", "back")
-
-    def __init__(self, t: torch.Tensor):
-        self.index = t.device.index
-
-    def __enter__(self):
-        self.back = None
-        if self.index is not None and torch.cuda.current_device() != self.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
 
 
 def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, rope_base: float,
@@ -743,18 +742,30 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
     """Writes a step's new rows [n_rows, h_kv, d] (rows of any stride) into their pages, keys
     rotated at pos0 + row_pos. Returns the workspace, whose status word a bad slot sets; pass
     the plan's as ``ws`` to read one status a step."""
-    _pool("paged_append", K_pages, V_pages)
-    h_kv, d = K_pages.shape[2:]
-    n_rows = K_new.shape[0]
-    _packed("paged_append", "K_new", K_new, n_rows, h_kv, d, K_pages)
-    _packed("paged_append", "V_new", V_new, n_rows, h_kv, d, K_pages)
-    _int32("paged_append", slot_map=slot_map, row_pos=row_pos)
-    _need("paged_append", slot_map.numel() >= n_rows and row_pos.numel() >= n_rows,
-          f"slot_map and row_pos cover {min(slot_map.numel(), row_pos.numel())} of {n_rows} rows")
     if ws is None:
         ws = torch.zeros(256, dtype=torch.uint8, device=K_pages.device)
-    _same("paged_append", K_pages, slot_map=slot_map, row_pos=row_pos, ws=ws)
-    with _on(K_pages):
+    dt, dev, i32 = K_pages.dtype, K_pages.get_device(), torch.int32
+    n_rows, h_kv, d = K_new.shape
+    if not (K_pages.dim() == 4 and K_pages.shape == V_pages.shape and
+            K_pages.shape[2:] == K_new.shape[1:] and K_new.shape == V_new.shape and
+            V_pages.dtype == dt and K_new.dtype == dt and V_new.dtype == dt and
+            slot_map.dtype == i32 and row_pos.dtype == i32 and
+            V_pages.get_device() == dev and K_new.get_device() == dev and
+            V_new.get_device() == dev and slot_map.get_device() == dev and
+            row_pos.get_device() == dev and ws.get_device() == dev and
+            K_pages.is_contiguous() and V_pages.is_contiguous() and slot_map.is_contiguous() and
+            row_pos.is_contiguous() and ws.is_contiguous() and
+            K_new.stride()[1:] == (d, 1) and V_new.stride()[1:] == (d, 1) and
+            slot_map.numel() >= n_rows and row_pos.numel() >= n_rows):
+        _explain_pool("paged_append", K_pages, V_pages)
+        shape = (n_rows, *K_pages.shape[2:])
+        _explain_rows("paged_append", "K_new", K_new, shape, K_pages)
+        _explain_rows("paged_append", "V_new", V_new, shape, K_pages)
+        _explain_arrays("paged_append", dev, slot_map=(slot_map, i32, None),
+                        row_pos=(row_pos, i32, None), ws=(ws, None, None))
+        rows = min(slot_map.numel(), row_pos.numel())
+        _need("paged_append", rows >= n_rows, f"slot_map and row_pos cover {rows} of {n_rows} rows")
+    with _on(dev):
         msa_paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, rope_base, ws,
                          stream)
     return ws
@@ -766,34 +777,57 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
     """Attention of every request's new tokens Q [n_rows, h_q, d] (packed by ``row_start``, rows
     of any stride) over [routed memory ; paged local context of ``length`` rows]; returns O
     [n_rows, h_q, d] (rows behind the last request's as they were)."""
-    _pool("paged_attend", K_pages, V_pages)
+    dt, dev, i32 = K_pages.dtype, K_pages.get_device(), torch.int32
     n_rows, h_q, d = Q.shape
     n_pages, page, h_kv, _ = K_pages.shape
     n_req, max_pages = block_table.shape
-    _packed("paged_attend", "Q", Q, n_rows, h_q, K_pages.shape[3], K_pages)
-    _int32("paged_attend", row_start=row_start, length=length, block_table=block_table,
-           ctx_len=ctx_len)
-    _need("paged_attend", row_start.numel() == n_req + 1 and length.numel() == n_req,
-          f"row_start and length do not fit {n_req} requests")
-    max_ctx = 0
-    if ctxK is not None:
-        max_ctx = ctxK.shape[1]
-        _need("paged_attend", ctxV is not None and ctx_len is not None and
-              ctx_len.numel() == n_req and ctxK.shape == ctxV.shape and
-              tuple(ctxK.shape) == (n_req, max_ctx, h_kv, d) and ctxK.dtype == Q.dtype and
-              ctxV.dtype == Q.dtype, "the memory is ctxK, ctxV [n_req, max_ctx, h_kv, d] and "
-                                     "ctx_len [n_req]")
+    max_ctx = 0 if ctxK is None else ctxK.shape[1]
     if O is None:
-        O = torch.empty((n_rows, h_q, d), dtype=Q.dtype, device=Q.device)
-    _need("paged_attend", O.shape == Q.shape and O.dtype == Q.dtype, "O is not like Q")
-    with _on(K_pages):
+        O = torch.empty((n_rows, h_q, d), dtype=dt, device=K_pages.device)
+    if not (K_pages.shape == V_pages.shape and K_pages.shape[3] == d and O.shape == Q.shape and
+            V_pages.dtype == dt and Q.dtype == dt and O.dtype == dt and
+            row_start.dtype == i32 and length.dtype == i32 and block_table.dtype == i32 and
+            V_pages.get_device() == dev and Q.get_device() == dev and O.get_device() == dev and
+            row_start.get_device() == dev and length.get_device() == dev and
+            block_table.get_device() == dev and
+            K_pages.is_contiguous() and V_pages.is_contiguous() and O.is_contiguous() and
+            row_start.is_contiguous() and length.is_contiguous() and
+            block_table.is_contiguous() and Q.stride()[1:] == (d, 1) and
+            row_start.numel() == n_req + 1 and length.numel() == n_req and
+            (ctxK is None or (
+                ctxV is not None and ctx_len is not None and
+                ctxK.shape == (n_req, max_ctx, h_kv, d) and ctxV.shape == ctxK.shape and
+                ctxK.dtype == dt and ctxV.dtype == dt and ctx_len.dtype == i32 and
+                ctx_len.numel() == n_req and ctxK.get_device() == dev and
+                ctxV.get_device() == dev and ctx_len.get_device() == dev and
+                ctxK.is_contiguous() and ctxV.is_contiguous() and ctx_len.is_contiguous()))):
+        what = "paged_attend"
+        _explain_pool(what, K_pages, V_pages)
+        _explain_rows(what, "Q", Q, (n_rows, h_q, K_pages.shape[3]), K_pages)
+        _need(what, O.shape == Q.shape and O.dtype == dt, "O is not like Q")
+        _need(what, ctxK is None or (
+            ctxV is not None and ctx_len is not None and ctxK.shape == ctxV.shape and
+            tuple(ctxK.shape) == (n_req, max_ctx, h_kv, d)),
+            "the memory is ctxK, ctxV [n_req, max_ctx, h_kv, d] and ctx_len [n_req]")
+        _explain_arrays(what, dev, O=(O, dt, None), row_start=(row_start, i32, n_req + 1),
+                        length=(length, i32, n_req), block_table=(block_table, i32, None),
+                        ctxK=(ctxK, dt, None), ctxV=(ctxV, dt, None),
+                        ctx_len=(ctx_len, i32, n_req))
+    with _on(dev):
         if ws is None:
             ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q),
                                                 max_ctx, max_pages, page), Q.device)
-        _same("paged_attend", K_pages, row_start=row_start, length=length, O=O, ws=ws,
-              block_table=block_table, ctxK=ctxK, ctxV=ctxV, ctx_len=ctx_len)
-        msa_paged_attend(Q, row_start, length, K_pages, V_pages, block_table, ctxK, ctxV, ctx_len,
-                         pos0, rope_base, scale, O, ws, stream)
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            _explain_arrays("paged_attend", dev, ws=(ws, None, None))
+        st = _s(stream)
+        status = lib.msa_paged_attend(
+            Q.data_ptr(), Q.stride(0), n_rows, h_q, row_start.data_ptr(), length.data_ptr(), n_req,
+            K_pages.data_ptr(), V_pages.data_ptr(), n_pages, page, block_table.data_ptr(),
+            max_pages, None if ctxK is None else ctxK.data_ptr(),
+            None if ctxK is None else ctxV.data_ptr(),
+            None if ctxK is None else ctx_len.data_ptr(), max_ctx, h_kv, d, dtype_code(Q), pos0,
+            rope_base, scale, O.data_ptr(), ws.data_ptr(), ws.nbytes, st)
+    _check(status)
     return O
 
 

@@ -167,12 +167,11 @@ size_t msa_paged_attend_workspace(int32_t n_rows, int32_t n_req, int32_t h_q, in
                                   int32_t page_size) {
   if (n_rows < 1 || n_req < 1 || h_kv < 1 || h_kv > kMaxHeads || h_q < h_kv || d < 1)
     return kHeader;
-  (void)dtype;
   (void)max_ctx;
   (void)max_pages;
   (void)page_size;
-  const msa::PagedPlan pl = msa::paged_attend_plan(n_req, h_kv, d, dtype, sm_count());
-  return kHeader + pl.err_bytes + pl.tail_bytes + pl.ml_bytes + pl.o_bytes;
+  return kHeader +
+         msa::paged_attend_plan(n_rows, n_req, h_q, h_kv, d, dtype, sm_count()).bytes();
 }
 
 msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
@@ -191,14 +190,18 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
   REQUIRE(n_rows >= 0 && (int64_t)n_rows * h_q < (1ll << 31) && max_ctx >= 0 && pos0 >= 0,
           MSA_ERR_INVALID_ARG, "bad sizes (n_rows=%d h_q=%d max_ctx=%d pos0=%d)", n_rows, h_q,
           max_ctx, pos0);
+  REQUIRE((int64_t)n_req * max_ctx < (1ll << 31), MSA_ERR_INVALID_ARG,
+          "n_req * max_ctx %lld (below 2^31)", (long long)n_req * max_ctx);
   REQUIRE(scale == scale && std::fabs(scale) <= 3.0e38f, MSA_ERR_INVALID_ARG,
           "scale is not finite");
-  const size_t need = msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype, max_ctx,
-                                                 max_pages, page_size);
+  const bool any = n_rows > 0 && n_req > 0;
+  msa::PagedPlan pl{};
+  if (any) pl = msa::paged_attend_plan(n_rows, n_req, h_q, h_kv, d, dtype, sm_count());
+  const size_t need = kHeader + pl.bytes();
   REQUIRE(ws != nullptr && ws_bytes >= need && aligned(ws, 256), MSA_ERR_WORKSPACE,
           "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, need);
   const int64_t per16 = 16 / (int64_t)esize(dtype);
-  if (n_rows > 0 && n_req > 0) {
+  if (any) {
     REQUIRE(Q && row_start && len && K_pages && V_pages && block_table && O, MSA_ERR_INVALID_ARG,
             "null tensor");
     REQUIRE(max_ctx == 0 || (ctxK && ctxV && ctx_len), MSA_ERR_INVALID_ARG, "null context");
@@ -209,7 +212,7 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
             MSA_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
   }
   cudaStream_t st = (cudaStream_t)stream;
-  if (n_rows == 0 || n_req == 0)  // nothing to do but to start the status word
+  if (!any)  // nothing to do but to start the status word
     return done(cudaMemsetAsync(ws, 0, sizeof(int32_t), st), "msa_paged_attend");
   msa::PagedAttendParams p{};
   p.Q = Q;
@@ -235,17 +238,22 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
   msa::rope_turns(p.rope ? (double)rope_base : 0.0, d, p.rope_turns);
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * 1.4426950408889634f;
   p.O = O;
-  const msa::PagedPlan pl = msa::paged_attend_plan(n_req, h_kv, d, dtype, sm_count());
   unsigned char* w8 = static_cast<unsigned char*>(ws);
-  p.err = reinterpret_cast<int*>(w8);
-  w8 += kHeader;
-  p.err_cta = reinterpret_cast<int*>(w8);
-  w8 += pl.err_bytes;
-  p.tail = reinterpret_cast<int4*>(w8);
-  w8 += pl.tail_bytes;
-  p.part_ml = reinterpret_cast<float*>(w8);
-  w8 += pl.ml_bytes;
-  p.part_o = reinterpret_cast<float*>(w8);
+  auto take = [&](size_t bytes) {
+    unsigned char* at = w8;
+    w8 += bytes;
+    return at;
+  };
+  p.err = reinterpret_cast<int*>(take(kHeader));
+  p.err_cta = reinterpret_cast<int*>(take(pl.err_bytes));
+  p.tail = reinterpret_cast<int4*>(take(pl.tail_bytes));
+  p.part_ml = reinterpret_cast<float*>(take(pl.ml_bytes));
+  p.part_o = reinterpret_cast<float*>(take(pl.o_bytes));
+  p.tc_tail = reinterpret_cast<int4*>(take(pl.tc_tail_bytes));
+  p.tc_ml = reinterpret_cast<float*>(take(pl.tc_ml_bytes));
+  p.tc_o = reinterpret_cast<float*>(take(pl.tc_o_bytes));
+  p.tc_rows = pl.tc_grid > 0 ? msa::kPagedWarpRows : INT32_MAX;
+  p.tc_err_at = pl.grid;
   return done(msa::launch_paged_attend(p, pl, dtype, d, st), "msa_paged_attend launch");
 }
 

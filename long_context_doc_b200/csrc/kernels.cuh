@@ -360,6 +360,7 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, in
                                 cudaStream_t st);
 
 // ---- paged_attend.cu: attention of ragged requests over [routed memory ; paged local context]
+constexpr int kPagedWarpRows = 16;  // query rows per KV head of a block of the warp-level kernel
 struct PagedAttendParams {
   const void* Q;            // [n_rows] rows of h_q * d elements, q_stride elements apart
   int64_t q_stride;
@@ -379,17 +380,28 @@ struct PagedAttendParams {
   float scale_log2;
   void* O;                  // [n_rows, h_q, d]
   int* err;                 // status word, written by the merge kernel
-  int* err_cta;             // [grid] what each CTA of the attention kernel recorded
-  int4* tail;               // [S] the item a split begins and does not end
-  float* part_ml;           // [S][2][h_kv][rows][2]
-  float* part_o;            // [S][2][h_kv][rows][d]
+  int* err_cta;             // what each CTA recorded: [grid], then [tc_grid]
+  int4* tail;               // [S] the item a range begins and does not end
+  float* part_ml;           // [S][2][h_kv][16][2] partials of the warp-level kernel
+  float* part_o;            // [S][2][h_kv][16][d]
+  int tc_rows;              // requests with more query rows per KV head take the tcgen05 kernel
+  int tc_err_at;            // its first entry of err_cta
+  int4* tc_tail;            // [tc_grid][2]
+  float* tc_ml;             // [tc_grid][2][256][2] its partials
+  float* tc_o;              // [tc_grid][2][256][d]
 };
 struct PagedPlan {
   int grid, S;              // CTAs; ranges that the tile list is cut into (per KV head)
-  size_t err_bytes, tail_bytes, ml_bytes, o_bytes, smem;
+  int tc_grid;              // CTAs of the tcgen05 kernel (0: not launched)
+  size_t err_bytes, tail_bytes, ml_bytes, o_bytes, tc_tail_bytes, tc_ml_bytes, tc_o_bytes, smem;
+  size_t bytes() const {
+    return err_bytes + tail_bytes + ml_bytes + o_bytes + tc_tail_bytes + tc_ml_bytes + tc_o_bytes;
+  }
 };
-PagedPlan paged_attend_plan(int n_req, int h_kv, int d, int dtype, int sms);
+PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int dtype, int sms);
 cudaError_t launch_paged_attend(const PagedAttendParams& p, const PagedPlan& pl, int dtype, int d,
                                 cudaStream_t st);
+// ---- paged_attend_tc.cu (bf16), launched between the warp-level kernel and the merge
+cudaError_t launch_paged_attend_tc(const PagedAttendParams& p, int grid, int d, cudaStream_t st);
 
 }  // namespace msa

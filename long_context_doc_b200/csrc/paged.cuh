@@ -1,0 +1,33 @@
+// paged.cuh - what the kernels of the paged attention share: a request's geometry on the device.
+#pragma once
+
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace msa {
+
+struct PagedReq {
+  int a, T, L, C;  // first row, new tokens, local rows, memory rows
+};
+
+// Request r if it has more than `lo` and at most `hi` query rows per KV head, else one without
+// tokens. A length out of range and row starts that decrease or pass n_rows are recorded in
+// *bad, and the request is left out (its rows of O are not written).
+__device__ __forceinline__ PagedReq paged_req(const PagedAttendParams& p, int r, int lo, int hi,
+                                              int* bad) {
+  PagedReq q;
+  q.a = __ldg(p.row_start + r);
+  q.T = __ldg(p.row_start + r + 1) - q.a;
+  q.L = __ldg(p.len + r);
+  q.C = p.ctx_len != nullptr ? min(max(__ldg(p.ctx_len + r), 0), p.max_ctx) : 0;
+  const bool ok = q.a >= 0 && q.T >= 0 && q.T <= p.n_rows - q.a && q.L >= 0 &&
+                  q.L <= ((long long)p.max_pages << p.page_shift);
+  if (!ok) *bad = kErrBadIndex;
+  const int rows = ok ? q.T * (p.h_q / p.h_kv) : 0;  // n_rows * h_q is below 2^31
+  if (!ok || rows <= lo || rows > hi) q.a = q.T = q.L = q.C = 0;
+  return q;
+}
+
+}  // namespace msa

@@ -22,13 +22,14 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 namespace msa {
 namespace pga {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;           // query rows of a block (the MMA's M)
+constexpr int kRows = kPagedWarpRows;  // query rows of a block (the MMA's M)
 constexpr int kRing = 24576;        // bytes of a warp's ring
 constexpr int kMinTiles = 4;        // a range is at least this many tiles
 constexpr int kMergeThreads = 256;
@@ -97,30 +98,11 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
 }
 
-// What the step says about a request. Lengths out of range and row starts that decrease or
-// pass n_rows are recorded, and the request is left out (its rows of O are not written).
-struct Req {
-  int a, T, L, C;  // first row, new tokens, local rows, memory rows
-};
-__device__ __forceinline__ Req load_req(const PagedAttendParams& p, int r, int* bad) {
-  Req q;
-  q.a = __ldg(p.row_start + r);
-  q.T = __ldg(p.row_start + r + 1) - q.a;
-  q.L = __ldg(p.len + r);
-  q.C = p.ctx_len != nullptr ? min(max(__ldg(p.ctx_len + r), 0), p.max_ctx) : 0;
-  if (q.a < 0 || q.T < 0 || q.T > p.n_rows - q.a || q.L < 0 ||
-      q.L > ((long long)p.max_pages << p.page_shift)) {
-    *bad = kErrBadIndex;
-    q.a = q.T = q.L = q.C = 0;
-  }
-  return q;
-}
-
-template <int KT> __device__ __forceinline__ int ctx_tiles(const Req& q) {
+template <int KT> __device__ __forceinline__ int ctx_tiles(const PagedReq& q) {
   return (q.C + KT - 1) / KT;
 }
 // tiles of a query block (at least one, so that a block that sees nothing is still written)
-template <int KT> __device__ __forceinline__ int block_tiles(const Req& q) {
+template <int KT> __device__ __forceinline__ int block_tiles(const PagedReq& q) {
   return max(1, ctx_tiles<KT>(q) + (int)(((long long)q.L + KT - 1) / KT));
 }
 
@@ -155,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     const int r = r0 + tid;
     int64_t v = 0;
     if (r < p.n_req) {
-      const Req q = load_req(p, r, &err);
+      const PagedReq q = paged_req(p, r, 0, p.tc_rows, &err);
       v = (int64_t)(((long long)q.T * Gq + kRows - 1) / kRows) * block_tiles<KT>(q);
     }
     int64_t inc = v;
@@ -192,12 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     // where a tile of the list lies
     struct Cur {
       int r, blk, t, TPP, CT, nb;
-      Req q;
+      PagedReq q;
     };
     auto enter = [&](Cur& c, int r) {  // request r's geometry (r has tiles)
       int ignore = 0;
       c.r = r;
-      c.q = load_req(p, r, &ignore);
+      c.q = paged_req(p, r, 0, p.tc_rows, &ignore);
       c.CT = ctx_tiles<KT>(c.q);
       c.TPP = block_tiles<KT>(c.q);
       c.nb = (int)(((long long)c.q.T * Gq + kRows - 1) / kRows);
@@ -519,20 +501,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   if (tid == 0) p.err_cta[blockIdx.x] = cta_err;
 }
 
-// Partials of the query blocks that no single range held whole: block (s, head) folds the item
-// that range s begins and the ranges s + 1 .. tail.w go on with. The warps split the ranges
-// among them in the same way whatever the timing; out = sum_i 2^(m_i - M) o_i / sum_i ... l_i.
+// Partials of the query blocks that no single range held whole: the block that range s begins
+// and the ranges s + 1 .. tail.w go on with, out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
+// over its segments i in a fixed order. The first S * h_kv CTAs take the warp-level kernel's
+// blocks of 16 rows (a row's segments shared among the warps), kTcParts CTAs a range the tcgen05
+// kernel's blocks of up to 256 rows (a warp a row). Few bytes: latency-bound.
+template <int EL> struct Fold {
+  float M = -INFINITY, L = 0.f, acc[EL];
+  __device__ __forceinline__ Fold() {
+#pragma unroll
+    for (int e = 0; e < EL; ++e) acc[e] = 0.f;
+  }
+  // segments i, i + step, i + 2 step, .. < n, four loads in flight; slot(i): the row's partial
+  template <typename F>
+  __device__ __forceinline__ void run(int i, int step, int n, const float* ml, const float* o,
+                                      int lane, F slot) {
+    for (; i < n; i += step * 4) {
+      float mi[4], li[4], ov[4][EL];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = i + u * step;
+        mi[u] = -INFINITY;
+        li[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) ov[u][e] = 0.f;
+        if (j < n) {
+          const int64_t at = slot(j);
+          mi[u] = ml[at * 2];
+          li[u] = ml[at * 2 + 1];
+#pragma unroll
+          for (int e = 0; e < EL; ++e) ov[u][e] = o[at * (EL * 32) + e * 32 + lane];
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) Mn = fmaxf(Mn, mi[u]);
+      rescale(Mn);
+      const float use = Mn == -INFINITY ? 0.f : Mn;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = ex2(mi[u] - use);
+        L = fmaf(li[u], w, L);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) acc[e] = fmaf(ov[u][e], w, acc[e]);
+      }
+    }
+  }
+  __device__ __forceinline__ void rescale(float Mn) {
+    const float a = ex2(M - (Mn == -INFINITY ? 0.f : Mn));
+    L *= a;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) acc[e] *= a;
+    M = Mn;
+  }
+  template <typename T> __device__ __forceinline__ void store(T* out, int lane) const {
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) out[e * 32 + lane] = Elem<T>::from_f(acc[e] * inv);
+  }
+};
+constexpr int kTcParts = 32;  // CTAs per range of the tcgen05 kernel: 8 of its 256 rows each
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedAttendParams p,
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedAttendParams p, int S,
                                                                     int n_cta) {
   constexpr int EL = D / 32;  // elements a lane holds
-  __shared__ float sh_o[kMergeThreads / 32][D];
-  __shared__ float sh_m[kMergeThreads / 32], sh_l[kMergeThreads / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int s = blockIdx.x, head = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = kMergeThreads / 32;
-  if (s == 0 && head == 0) {  // the call's status word
+  __shared__ float sh_o[W][D];
+  __shared__ float sh_m[W], sh_l[W];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int Gq = p.h_q / p.h_kv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0) {  // the call's status word
     __shared__ int code;
     if (tid == 0) code = 0;
     __syncthreads();
@@ -541,82 +581,56 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedAttendP
     __syncthreads();
     if (tid == 0) *p.err = code;
   }
+  const int n_warp_level = S * p.h_kv;
+  if ((int)blockIdx.x >= n_warp_level) {
+    const int s = ((int)blockIdx.x - n_warp_level) / kTcParts;
+    const int row = ((int)blockIdx.x - n_warp_level) % kTcParts * W + warp;
+    const int4 tail = p.tc_tail[2 * s];
+    if (tail.x < 0) return;
+    const int head = p.tc_tail[2 * s + 1].x;
+    const int TB = 256 / Gq;
+    if (row >= min(TB, tail.y - tail.z * TB) * Gq) return;
+    Fold<EL> f;
+    f.run(0, 1, tail.w - s + 1, p.tc_ml, p.tc_o, lane, [&](int i) {
+      return ((int64_t)(s + i) * 2 + (i == 0 ? 1 : 0)) * 256 + row;
+    });
+    const int tok = tail.z * TB + row / Gq, hq = head * Gq + row % Gq;
+    f.store(static_cast<T*>(p.O) + ((int64_t)(tail.x + tok) * p.h_q + hq) * D, lane);
+    return;
+  }
+  const int s = blockIdx.x / p.h_kv, head = blockIdx.x % p.h_kv;
   const int4 tail = p.tail[s];
   if (tail.x < 0) return;
-  const int Gq = p.h_q / p.h_kv;
-  const int nrow = (int)min((long long)kRows, (long long)tail.y * Gq - (long long)tail.z * kRows);
-  // warps per row: a power of two, so that a row's warps are neighbours
-  int wpr = 1;
+  const int nrow = min(kRows, tail.y * Gq - tail.z * kRows);
+  int wpr = 1;  // warps per row: a power of two, so that a row's warps are neighbours
   while (wpr * 2 * nrow <= W) wpr *= 2;
-  const int n_seg = tail.w - s + 1;
   const int g = warp % wpr;
   for (int r0 = 0; r0 < nrow; r0 += W / wpr) {
     const int lr = r0 + warp / wpr;
     const bool live = lr < nrow;
-    auto slot = [&](int i) {  // segment i: the tail slot of s, then the head slots
-      return (((int64_t)(s + i) * 2 + (i == 0 ? 1 : 0)) * p.h_kv + head) * kRows + lr;
-    };
-    float M = -INFINITY, L = 0.f;
-    float acc[EL];
-#pragma unroll
-    for (int e = 0; e < EL; ++e) acc[e] = 0.f;
-    if (live) {
-      for (int i = g; i < n_seg; i += wpr * 4) {
-        float mi[4], li[4], ov[4][EL];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int j = i + u * wpr;
-          mi[u] = -INFINITY;
-          li[u] = 0.f;
-#pragma unroll
-          for (int e = 0; e < EL; ++e) ov[u][e] = 0.f;
-          if (j < n_seg) {
-            const int64_t at = slot(j);
-            mi[u] = p.part_ml[at * 2];
-            li[u] = p.part_ml[at * 2 + 1];
-#pragma unroll
-            for (int e = 0; e < EL; ++e) ov[u][e] = p.part_o[at * D + e * 32 + lane];
-          }
-        }
-        float Mn = M;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) Mn = fmaxf(Mn, mi[u]);
-        const float use = Mn == -INFINITY ? 0.f : Mn;
-        const float a = ex2(M - use);
-        L *= a;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) acc[e] *= a;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float w = ex2(mi[u] - use);
-          L = fmaf(li[u], w, L);
-#pragma unroll
-          for (int e = 0; e < EL; ++e) acc[e] = fmaf(ov[u][e], w, acc[e]);
-        }
-        M = Mn;
-      }
-    }
+    Fold<EL> f;
+    if (live)  // the tail slot of s, then the head slots
+      f.run(g, wpr, tail.w - s + 1, p.part_ml, p.part_o, lane, [&](int i) {
+        return (((int64_t)(s + i) * 2 + (i == 0 ? 1 : 0)) * p.h_kv + head) * kRows + lr;
+      });
     if (wpr > 1) {
 #pragma unroll
-      for (int e = 0; e < EL; ++e) sh_o[warp][e * 32 + lane] = acc[e];
+      for (int e = 0; e < EL; ++e) sh_o[warp][e * 32 + lane] = f.acc[e];
       if (lane == 0) {
-        sh_m[warp] = M;
-        sh_l[warp] = L;
+        sh_m[warp] = f.M;
+        sh_l[warp] = f.L;
       }
       __syncthreads();
       if (g == 0) {
-        float Mn = M;
+        float Mn = f.M;
         for (int u = 1; u < wpr; ++u) Mn = fmaxf(Mn, sh_m[warp + u]);
+        f.rescale(Mn);
         const float use = Mn == -INFINITY ? 0.f : Mn;
-        const float a = ex2(M - use);
-        L *= a;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) acc[e] *= a;
         for (int u = 1; u < wpr; ++u) {
           const float w = ex2(sh_m[warp + u] - use);
-          L = fmaf(sh_l[warp + u], w, L);
+          f.L = fmaf(sh_l[warp + u], w, f.L);
 #pragma unroll
-          for (int e = 0; e < EL; ++e) acc[e] = fmaf(sh_o[warp + u][e * 32 + lane], w, acc[e]);
+          for (int e = 0; e < EL; ++e) f.acc[e] = fmaf(sh_o[warp + u][e * 32 + lane], w, f.acc[e]);
         }
       }
       __syncthreads();
@@ -624,10 +638,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedAttendP
     if (live && g == 0) {
       const int row = tail.z * kRows + lr;
       const int tok = row / Gq, hq = head * Gq + row % Gq;
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      T* out = static_cast<T*>(p.O) + ((int64_t)(tail.x + tok) * p.h_q + hq) * D;
-#pragma unroll
-      for (int e = 0; e < EL; ++e) out[e * 32 + lane] = Elem<T>::from_f(acc[e] * inv);
+      f.store(static_cast<T*>(p.O) + ((int64_t)(tail.x + tok) * p.h_q + hq) * D, lane);
     }
   }
 }
@@ -641,9 +652,13 @@ cudaError_t launch(const PagedAttendParams& p, const PagedPlan& pl, cudaStream_t
   kfn<<<pl.grid, kThreads, pl.smem, st>>>(p, pl.S);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if constexpr (sizeof(T) == 2) {  // its CTAs start as the warp-level kernel's end
+    if (pl.tc_grid > 0) e = launch_paged_attend_tc(p, pl.tc_grid, D, st);
+    if (e != cudaSuccess) return e;
+  }
   // the merge kernel is launched while the attention runs and waits for it on the device
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pl.S, p.h_kv);
+  cfg.gridDim = dim3(pl.S * p.h_kv + pl.tc_grid * kTcParts);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -651,22 +666,33 @@ cudaError_t launch(const PagedAttendParams& p, const PagedPlan& pl, cudaStream_t
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, p, pl.grid);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, p, pl.S, pl.grid + pl.tc_grid);
 }
 
 }  // namespace pga
 
-PagedPlan paged_attend_plan(int n_req, int h_kv, int d, int dtype, int sms) {
+PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int dtype, int sms) {
   PagedPlan pl{};
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   // one CTA per SM; more when the heads alone need more warps
   pl.grid = std::max(sms, (h_kv + pga::kWarps - 1) / pga::kWarps);
   pl.S = pl.grid * pga::kWarps / h_kv;
+  // The tcgen05 kernel serves the bf16 requests with more than 16 query rows per KV head. The
+  // host sees only the totals: it leaves the launch out where no request can have so many, and
+  // where there is at most one new token per request on average (a decode step, where the launch
+  // would cost its latency and find nothing; the warp-level kernel serves a longer request too).
+  const int Gq = h_q / h_kv;
+  const bool tc = dtype == 1 && Gq <= 256 && (int64_t)n_rows * Gq > kPagedWarpRows &&
+                  n_rows > n_req;
+  pl.tc_grid = tc ? sms : 0;
   const size_t slots = (size_t)pl.S * 2 * h_kv * pga::kRows;
-  pl.err_bytes = al((size_t)pl.grid * sizeof(int));
+  pl.err_bytes = al((size_t)(pl.grid + pl.tc_grid) * sizeof(int));
   pl.tail_bytes = al((size_t)pl.S * sizeof(int4));
   pl.ml_bytes = al(slots * 2 * sizeof(float));
   pl.o_bytes = al(slots * d * sizeof(float));
+  pl.tc_tail_bytes = al((size_t)pl.tc_grid * 2 * sizeof(int4));
+  pl.tc_ml_bytes = al((size_t)pl.tc_grid * 2 * 256 * 2 * sizeof(float));
+  pl.tc_o_bytes = al((size_t)pl.tc_grid * 2 * 256 * d * sizeof(float));
   pl.smem = pga::kWarps * pga::kRing + ((size_t)n_req + 1) * sizeof(int64_t);
   return pl;
 }

@@ -303,7 +303,7 @@ def test_helpers_refuse_what_pointers_cannot_show(msa):
         msa.paged_append(pool, pool, i32(2), i32(3), torch.zeros(3, 2, 64),
                          torch.zeros(3, 2, 64), 0, 0.0)
     Q = torch.zeros(5, 4, 64)
-    with pytest.raises(msa.MSAError, match="do not fit"):
+    with pytest.raises(msa.MSAError, match="row_start has 2"):
         msa.paged_attend(Q, i32(2), i32(2), pool, pool, i32(2, 3), 0, 0.0)
     with pytest.raises(msa.MSAError, match="the memory is"):
         msa.paged_attend(Q, i32(3), i32(2), pool, pool, i32(2, 3), 0, 0.0,
