@@ -13,8 +13,10 @@
 // stored. Warps 2-9 hold one query row per thread: they rotate and stage their half's queries,
 // load the 128 scores of a tile from TMEM once, mask, and keep the running maximum (raised, with
 // O rescaled in TMEM, only when a tile's maximum passes it by more than 8 in log2 units) and sum
-// in fp32. A half's completed scores imply its earlier products (the issuing thread's MMAs
-// complete in order), so O is rescaled and Q replaced without further waits.
+// in fp32. With two halves a half's completed scores imply its earlier products (the issuing
+// thread's MMAs complete in order), so O is rescaled and Q replaced without further waits. A
+// block of one half has both scores buffers to itself: the scores of a tile are formed before
+// the product of the tile before it.
 // Every wait is bounded; on expiry the CTA records kErrWaitTimeout, lets its copies and MMAs
 // land, frees its TMEM and leaves the rest unwritten.
 #include <cuda.h>
@@ -65,28 +67,35 @@ __device__ __forceinline__ uint64_t desc_mn(const void* rows) {
   const uint64_t a = (uint64_t)(smem_u32(rows) & 0x3FFFFu) >> 4;
   return a | ((uint64_t)(kSlice >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
+// The MMAs and commits are issued by one elected thread of a converged warp (always the same
+// one), so that their operands are computed in uniform registers: issued under a branch on the
+// lane, each operand's move into a uniform register made a 128 x 128 x 16 step take 137 clocks
+// instead of the tensor cores' 64.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
           smem_u32(bar))
       : "memory");
 }
+// a value that every lane of the warp holds, as one the compiler knows to be so
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -102,17 +111,34 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -126,13 +152,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Bounded wait by polling (a phase is usually a microsecond or less away): gives up after
+// 2^26 polls, a second or more, or when another role has given up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t par, int* err,
                                               volatile int* abort_flag) {
-  if (mbar_try_wait(bar, par)) return true;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, par)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kDefaultWaitLimit) {
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_test_wait(bar, par); ++i) {
+    if ((i & 63u) == 0u && *abort_flag) return false;
+    if (i >> 26) {
       set_err(err, kErrWaitTimeout);
       *abort_flag = 1;
       return false;
@@ -151,25 +178,51 @@ struct Work {
   int n_tiles;
   int rows;          // query rows of the block
 };
+struct Share {
+  int64_t x1, total;  // end of this CTA's share, tiles of the list
+  int G;              // shares
+};
 struct Walk {
   const PagedAttendParams& p;
   int Gq, TB;
-  int64_t left;      // tiles of the share still to hand out
+  int left;          // tiles of the share still to hand out
   __device__ __forceinline__ int blocks(const PagedReq& q) const { return (q.T + TB - 1) / TB; }
   __device__ __forceinline__ int tiles(const PagedReq& q, int blk) const {
     const int last = q.L - q.T + min(q.T, (blk + 1) * TB);  // rows the last token sees
     return max(1, (q.C + kN - 1) / kN + (max(last, 0) + kN - 1) / kN);
   }
-  __device__ __forceinline__ int64_t request_tiles(const PagedReq& q) const {  // of one KV head
-    int64_t n = 0;
-    for (int b = 0, nb = blocks(q); b < nb; ++b) n += tiles(q, b);
-    return n;
+  // Tiles of the request's first n blocks of one KV head. Of full blocks it is
+  // n CT + sum_{b < n} floor((x + TB b) / 128) with x = L - T + TB + 127, a sum of floors
+  // that needs no loop where TB divides 128 or is a multiple of it.
+  __device__ __forceinline__ int64_t first_blocks(const PagedReq& q, int n) const {
+    int64_t sum = 0;
+    int b = 0;
+    const int full = min(n, q.T / TB);
+    const int x = q.L - q.T + TB + kN - 1, ct = (q.C + kN - 1) / kN;
+    if (full > 2 && q.L >= q.T) {
+      if (TB % kN == 0) {
+        sum = (int64_t)full * (ct + x / kN) + (int64_t)(TB / kN) * full * (full - 1) / 2;
+        b = full;
+      } else if (kN % TB == 0) {
+        // with x = 128 e + TB u + v, v < TB, block b has e + floor((u + b) / (128 / TB))
+        const int per = kN / TB, u = x % kN / TB;
+        const int64_t end = u + full, whole = end / per;  // sum of floor(i / per), u <= i < end
+        sum = (int64_t)full * (ct + x / kN) + per * (whole * (whole - 1) / 2) +
+              whole * (end - whole * per);
+        b = full;
+      }
+    }
+    for (; b < n; ++b) sum += tiles(q, b);
+    return sum;
+  }
+  __device__ __forceinline__ int64_t request_tiles(const PagedReq& q) const {
+    return first_blocks(q, blocks(q));
   }
   __device__ __forceinline__ void set(Work& w, int from) {
     w.n_tiles = tiles(w.q, w.blk);
     w.rows = min(TB, w.q.T - w.blk * TB) * Gq;
     w.t0 = from;
-    w.t1 = (int)min((int64_t)w.n_tiles, from + left);
+    w.t1 = min(w.n_tiles, from + left);
     left -= w.t1 - from;
   }
   __device__ __forceinline__ void enter(Work& w, int r) {
@@ -184,9 +237,15 @@ struct Walk {
     enter(w, r);
     const int64_t per_head = request_tiles(w.q);
     w.head = (int)(off / per_head);
-    int64_t rem = off % per_head;
-    for (w.blk = 0; rem >= tiles(w.q, w.blk); ++w.blk) rem -= tiles(w.q, w.blk);
-    set(w, (int)rem);
+    const int64_t rem = off % per_head;
+    int lo = 0, hi = w.nb;  // first_blocks(lo) <= rem < first_blocks(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first_blocks(w.q, mid) <= rem) lo = mid;
+      else hi = mid;
+    }
+    w.blk = lo;
+    set(w, (int)(rem - first_blocks(w.q, lo)));
   }
   // The next block (whole warps; called only while left > 0, so there is one).
   __device__ __forceinline__ void next(Work& w, int lane) {
@@ -227,16 +286,23 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + NS * C::kTile);
   uint64_t* full = bars;            // [NS] ring tile landed
   uint64_t* empty = bars + NS;      // [NS] ring tile consumed
+  // (each with one waiting party that sees every phase: entry 2 is half 0's, for the tiles of a
+  // one-half block that use the second scores buffer)
   uint64_t* qfull = bars + 2 * NS;  // [2] a half's queries staged (128 threads)
-  uint64_t* sfull = qfull + 2;      // [2] a half's scores written
-  uint64_t* pfull = qfull + 4;      // [2] a half's probabilities written (128 threads)
-  uint64_t* odone = qfull + 6;      // [2] a block's last P V of the half completed
-  uint64_t* done = qfull + 8;       // every issued MMA completed
+  uint64_t* sfull = qfull + 2;      // [3] scores written
+  uint64_t* pfull = qfull + 5;      // [3] probabilities written (128 threads)
+  uint64_t* odone = qfull + 8;      // [2] a block's last P V of the half completed
+  uint64_t* pdone = qfull + 10;     // a P V of a one-half block completed
+  uint64_t* done = qfull + 11;      // every issued MMA completed
   __shared__ int64_t warp_tot[kThreads / 32];
   __shared__ int64_t start_off;
   __shared__ int start_r, cta_err;
   __shared__ int abort_word;
   __shared__ uint32_t tmem_holder;
+  __shared__ Work blocks[8];
+  __shared__ Share share;
+  __shared__ int4 tail_item;
+  __shared__ int tail_head;
   volatile int* abort_flag = &abort_word;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -250,13 +316,18 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&qfull[h], kHalf);
-      mbar_init(&sfull[h], 1);
-      mbar_init(&pfull[h], kHalf);
       mbar_init(&odone[h], 1);
     }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], kHalf);
+    }
+    mbar_init(pdone, 1);
     mbar_init(done, 1);
     abort_word = 0;
     cta_err = 0;
+    tail_item = make_int4(-1, 0, 0, 0);
+    tail_head = 0;
     start_r = -1;
     fence_mbar_init();
   }
@@ -307,9 +378,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   const bool work = (int)blockIdx.x < G;   // then start_r is set
   const int64_t x0 = work ? total * blockIdx.x / G : 0;
   const int64_t x1 = work ? total * (blockIdx.x + 1) / G : 0;
-  walk.left = x1 - x0;
-  int4 tail = make_int4(-1, 0, 0, 0);
-  int tail_head = 0;
+  walk.left = (int)(x1 - x0);
+  if (tid == 0) share = Share{x1, total, G};
 
   if (work) {
     if (warp == 0) {  // scores of the halves at columns 0 and 128, accumulators at 256 and 384
@@ -359,6 +429,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           }
           const uint32_t bytes =
               __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)rows_per * 128u;
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++seq) {
             const int s = seq % NS;
             if (seq >= NS) {
@@ -382,92 +453,133 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
         mbar_wait_bounded(&full[q % NS], (q / NS) & 1, &cta_err);
     } else if (warp == 1) {
-      // ---------------- MMA issuer
+      // ---------------- MMA issuer: the warp stays converged, see mma_ss
       constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) |
                                    ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
       constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
                                    ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
-      uint32_t seq = 0;              // next ring tile
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      constexpr uint32_t kStep = C::kTile >> 4;  // ring tile in descriptor units
+      const uint64_t q_desc = desc_k(q_s), k_desc = desc_k(ring), v_desc = desc_mn(ring);
+      int rs = 0;                    // next ring tile's stage and phase
+      uint32_t rp = 0;
+      uint32_t nq[2] = {0, 0}, np[3] = {0, 0, 0};
       auto wait = [&](uint64_t* bar, uint32_t par) {
-        return __all_sync(0xffffffffu, wait_or_abort(bar, par, &cta_err, abort_flag));
+        return uniform(wait_or_abort(bar, par, &cta_err, abort_flag)) != 0;
       };
-      auto wait_ring = [&](uint32_t q) { return wait(&full[q % NS], (q / NS) & 1); };
-      auto scores = [&](int h, uint32_t q) {  // S_h = Q_h K^T
-        fence_after();
-        if (lane == 0) {
-          const unsigned char* k = ring + (q % NS) * C::kTile;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk)
-            mma_ss(tmem + h * 128, desc_k(q_s + h * C::kTile + (kk >> 2) * kSlice) + 2 * (kk & 3),
-                   desc_k(k + (kk >> 2) * kSlice) + 2 * (kk & 3), idesc_s, kk ? 1u : 0u);
-          commit(&sfull[h]);
+      auto wait_ring = [&]() { return wait(&full[rs], rp); };
+      auto advance = [&]() {
+        if (++rs == NS) {
+          rs = 0;
+          rp ^= 1;
         }
-        __syncwarp();
       };
-      auto product = [&](int h, uint32_t q, bool first) {  // O_h (+)= P_h V
+      auto scores = [&](int h, int slot, int bar, int st) {  // S[slot] = Q_h K^T
         fence_after();
-        if (lane == 0) {
-          const unsigned char* v = ring + (q % NS) * C::kTile;
+        const uint64_t a = q_desc + h * kStep, b = k_desc + st * kStep;
 #pragma unroll
-          for (int kk = 0; kk < kN / 16; ++kk)
-            mma_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, desc_mn(v + kk * 2048), idesc_o,
-                   (first && kk == 0) ? 0u : 1u);
+        for (int kk = 0; kk < KS; ++kk) {  // 16 dims a step: 32 bytes of a row, 64 dims a slice
+          const uint32_t off = (kk >> 2) * (kSlice >> 4) + 2 * (kk & 3);
+          mma_ss(tmem + slot * 128, a + off, b + off, idesc_s, kk ? 1u : 0u);
         }
-        __syncwarp();
+        commit(&sfull[bar]);
       };
-      auto release = [&](uint32_t q) {
-        if (lane == 0) commit(&empty[q % NS]);
-        __syncwarp();
+      auto product = [&](int h, int slot, int st, bool first) {  // O_h (+)= P[slot] V
+        fence_after();
+        const uint64_t b = v_desc + st * kStep;
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)  // 16 keys a step
+          mma_ts(tmem + 256 + h * 128, tmem + slot * 128 + kk * 8, b + kk * (2048 >> 4), idesc_o,
+                 (first && kk == 0) ? 0u : 1u);
       };
       bool ok = true;
-      while (ok) {
-        const int nh = w.rows > kHalf ? 2 : 1;
-        const int n = w.t1 - w.t0;
-        ok = wait_ring(seq);
-        for (int h = 0; ok && h < nh; ++h) {
-          ok = wait(&qfull[h], nq[h] & 1);
-          ++nq[h];
-          if (ok) scores(h, seq);
-        }
-        if (!ok) break;
-        release(seq);
-        ++seq;
-        for (int j = 0; ok && j < n; ++j) {
-          const bool last = j + 1 == n;
-          for (int h = 0; ok && h < nh; ++h) {
-            ok = wait(&pfull[h], np[h] & 1);
-            ++np[h];
-            if (ok && h == 0) ok = wait_ring(seq);
+      while (true) {
+        const int n = uniform(w.t1 - w.t0);
+        if (uniform(w.rows) > kHalf) {
+          // two halves in alternation, each with its own scores
+          ok = wait_ring();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(&qfull[h], nq[h] & 1);
+            ++nq[h];
+            if (ok) scores(h, h, h, rs);
+          }
+          if (!ok) break;
+          commit(&empty[rs]);
+          advance();
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const bool last = j + 1 == n;
+            const int v = rs;
+            ok = wait(&pfull[0], np[0] & 1) && wait_ring();
+            ++np[0];
             if (!ok) break;
-            product(h, seq, j == 0);
-            if (h == nh - 1) release(seq);
+            product(0, 0, v, j == 0);
+            advance();
             if (last) {
-              if (lane == 0) commit(&odone[h]);
-              __syncwarp();
+              commit(&odone[0]);
             } else {
-              if (h == 0) ok = wait_ring(seq + 1);
+              ok = wait_ring();
               if (!ok) break;
-              scores(h, seq + 1);
-              if (h == nh - 1) release(seq + 1);
+              scores(0, 0, 0, rs);
+            }
+            ok = wait(&pfull[1], np[1] & 1);
+            ++np[1];
+            if (!ok) break;
+            product(1, 1, v, j == 0);
+            commit(&empty[v]);
+            if (last) {
+              commit(&odone[1]);
+            } else {
+              scores(1, 1, 1, rs);
+              commit(&empty[rs]);
+              advance();
             }
           }
-          seq += last ? 1 : 2;
+        } else {
+          // one half: its scores alternate between both buffers, a tile ahead of the products
+          ok = wait_ring() && wait(&qfull[0], nq[0] & 1);
+          ++nq[0];
+          if (!ok) break;
+          scores(0, 0, 0, rs);
+          commit(&empty[rs]);
+          advance();
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const int slot = j & 1;
+            const int v = rs;
+            const uint32_t vp = rp;
+            advance();
+            if (j + 1 < n) {
+              ok = wait_ring();
+              if (!ok) break;
+              scores(0, slot ^ 1, slot ? 0 : 2, rs);
+              commit(&empty[rs]);
+              advance();
+            }
+            ok = wait(&pfull[2 * slot], (slot ? np[2] : np[0]) & 1) && wait(&full[v], vp);
+            if (slot) ++np[2];
+            else ++np[0];
+            if (!ok) break;
+            product(0, slot, v, j == 0);
+            commit(&empty[v]);
+            commit(pdone);
+            if (j + 1 == n) commit(&odone[0]);
+          }
         }
         if (!ok || walk.left == 0) break;
         walk.next(w, lane);
       }
-      if (lane == 0) commit(done);
-      __syncwarp();
+      commit(done);
       mbar_wait_bounded(done, 0, &cta_err);
     } else {
       // ---------------- softmax: a half's 128 rows, one a thread
       const int h = (warp - 2) >> 2;
       const int lrow = (warp & 3) * 32 + lane;        // row in the half = TMEM lane
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t s_col = lane_base + h * 128, o_col = lane_base + 256 + h * 128;
+      const uint32_t o_col = lane_base + 256 + h * 128;
       const float c = p.scale_log2;
-      uint32_t nt = 0, nblk = 0;   // tiles and blocks this half has taken
+      uint32_t n_own = 0, n_alt = 0;  // phases of sfull[h], of sfull[2]
+      uint32_t no = 0, npd = 0;       // of odone[h], of pdone
       uint32_t seq = 0;            // ring tile of the block's first K
       auto wait = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, par, &cta_err, abort_flag));
@@ -479,37 +591,59 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         constexpr int LPR = D / 4;             // lanes a row takes
         constexpr int RPS = 32 / LPR;          // rows at once
         const int l = lane % LPR;
-        const int64_t pos0 = (int64_t)p.pos0 + b.q.L - b.q.T;
+        int64_t pos0 = (int64_t)p.pos0 + b.q.L - b.q.T;
         const unsigned long long F0 = p.rope_turns[2 * l], F1 = p.rope_turns[2 * l + 1];
-        int last_tok = -1;
-        float2 c0 = make_float2(1.f, 0.f), c1 = c0;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += RPS) {
-          const int rr = (warp & 3) * 32 + i + lane / LPR;   // row in the half
-          const int row = h * kHalf + rr;
-          if (row < b.rows) {
-            const int tok = b.blk * walk.TB + row / Gq;
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) +
-                                       (int64_t)(b.q.a + tok) * p.q_stride +
-                                       (b.head * Gq + row % Gq) * D;
-            const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(src) + l);
-            const uint32_t hi = __ldg(reinterpret_cast<const uint32_t*>(src + D / 2) + l);
-            if (p.rope && tok != last_tok) {
-              last_tok = tok;
+        const int row0 = h * kHalf + (warp & 3) * 32;          // the warp's first row
+        if (row0 < b.rows) {
+          int g = (row0 + lane / LPR) % Gq;                    // the lane's row, step by step
+          int tok = (row0 + lane / LPR) / Gq;
+          const int last_tok = (b.rows - 1) / Gq;              // rows past the block's repeat a
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) +  // row of its last
+                                     (int64_t)(b.q.a + b.blk * walk.TB) * p.q_stride +  // token
+                                     b.head * Gq * D;
+          constexpr int NI = 32 / RPS;
+          uint32_t lo[NI], hi[NI];
+          int tk = min(tok, last_tok), gk = g;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const uint32_t* at =
+                reinterpret_cast<const uint32_t*>(src + (int64_t)tk * p.q_stride + gk * D);
+            lo[i] = __ldg(at + l);
+            hi[i] = __ldg(at + D / 4 + l);
+            gk += RPS;
+            while (gk >= Gq) {
+              gk -= Gq;
+              tk = min(tk + 1, last_tok);
+            }
+          }
+          pos0 += b.blk * walk.TB;
+          int have = -1;
+          float2 c0 = make_float2(1.f, 0.f), c1 = c0;
+          unsigned char* row = q_s + h * C::kTile + ((warp & 3) * 32 + lane / LPR) * 128;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            if (p.rope && tok != have) {
+              have = tok;
               c0 = rot_turns(pos0 + tok, F0);
               c1 = rot_turns(pos0 + tok, F1);
             }
-            const float a0 = __uint_as_float(lo << 16), a1 = __uint_as_float(lo & 0xFFFF0000u);
-            const float b0 = __uint_as_float(hi << 16), b1 = __uint_as_float(hi & 0xFFFF0000u);
+            const float a0 = __uint_as_float(lo[i] << 16), a1 = __uint_as_float(lo[i] & 0xFFFF0000u);
+            const float b0 = __uint_as_float(hi[i] << 16), b1 = __uint_as_float(hi[i] & 0xFFFF0000u);
             const uint32_t ra = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
             const uint32_t rb = pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
-            unsigned char* dst = q_s + h * C::kTile + rr * 128;
-            // element e of the row: slice e / 64, 16-byte chunk (e % 64) / 8 ^ (row & 7)
+            // element e of row r: slice e / 64, 16-byte chunk (e % 64) / 8 ^ (r & 7)
+            unsigned char* dst = row + i * RPS * 128;
+            const int x = (lane / LPR + i * RPS) & 7;
             const int ea = 2 * l, eb = 2 * l + D / 2;
-            *reinterpret_cast<uint32_t*>(dst + (ea >> 6) * kSlice +
-                                         ((((ea & 63) >> 3) ^ (rr & 7)) << 4) + (ea & 7) * 2) = ra;
-            *reinterpret_cast<uint32_t*>(dst + (eb >> 6) * kSlice +
-                                         ((((eb & 63) >> 3) ^ (rr & 7)) << 4) + (eb & 7) * 2) = rb;
+            *reinterpret_cast<uint32_t*>(dst + (ea >> 6) * kSlice + ((((ea & 63) >> 3) ^ x) << 4) +
+                                         (ea & 7) * 2) = ra;
+            *reinterpret_cast<uint32_t*>(dst + (eb >> 6) * kSlice + ((((eb & 63) >> 3) ^ x) << 4) +
+                                         (eb & 7) * 2) = rb;
+            g += RPS;
+            while (g >= Gq) {
+              g -= Gq;
+              ++tok;
+            }
           }
         }
         fence_proxy_async_smem();
@@ -517,84 +651,105 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       };
       bool ok = true;
       if (h == 0 || w.rows > kHalf) stage_q(w);
-      while (ok) {
-        const bool active = h == 0 || w.rows > kHalf;
-        const int n = w.t1 - w.t0;
-        const bool begins = w.t0 == 0, ends = w.t1 == w.n_tiles;
-        const Work b = w;
+      while (true) {
+        // The block's geometry is kept in shared memory for its end and the walk: the tile loop
+        // holds a row of scores in registers.
+        if (lane == 0) blocks[warp - 2] = w;
+        __syncwarp();
+        const bool two = w.rows > kHalf;
+        const bool active = h == 0 || two;
+        const int t0 = w.t0, t1 = w.t1, CT = w.CT, n_ctx = w.q.C, n_loc = w.q.L;
         const bool more = walk.left > 0;
-        float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+        const bool any_row = h * kHalf + (warp & 3) * 32 < w.rows;  // of the warp
+        float m = -INFINITY, l = 0.f;
         if (active) {
           const int row = h * kHalf + lrow;
-          const bool any_row = h * kHalf + (warp & 3) * 32 < b.rows;  // of the warp
-          const int tok = b.blk * walk.TB + min(row, b.rows - 1) / Gq;
-          const int vis = b.q.L - b.q.T + tok;                        // last visible local row
-          const int vis_first = b.q.L - b.q.T + b.blk * walk.TB + h * kHalf / Gq;
-          for (int t = b.t0; t < b.t1; ++t, ++nt) {
-            const bool ctx = t < b.CT;
-            const int k0 = (ctx ? t : t - b.CT) * kN;
-            const int valid = (ctx ? b.q.C : b.q.L) - k0;            // rows the tile holds
-            ok = wait(&sfull[h], nt & 1);
+          // last visible local row of this row and of the half's first
+          const int vis = n_loc - w.q.T + w.blk * walk.TB + min(row, w.rows - 1) / Gq;
+          const int vis_first = min(n_loc - w.q.T + w.blk * walk.TB + h * kHalf / Gq, n_loc - 1);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          for (int t = t0; t < t1; ++t) {
+            const bool ctx = t < CT;
+            const int k0 = (ctx ? t : t - CT) * kN;
+            const int valid = (ctx ? n_ctx : n_loc) - k0;            // rows the tile holds
+            const bool alt = !two && ((t - t0) & 1);   // the second scores buffer
+            const int bar = alt ? 2 : h;
+            const uint32_t s_col = lane_base + (alt ? 128 : h * 128);
+            ok = wait(&sfull[bar], (alt ? n_alt++ : n_own++) & 1);
             if (!ok) break;
             fence_after();
             if (any_row) {
-              uint32_t sr[128];
+              float sr[128];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) ld32(s_col + i * 32, sr + i * 32);
+              for (int i = 0; i < 4; ++i)
+                ld32(s_col + i * 32, reinterpret_cast<uint32_t*>(sr) + i * 32);
               wait_ld();
-              if (!(ctx ? valid >= kN : k0 + kN - 1 <= min(vis_first, b.q.L - 1))) {
+              if (!(ctx ? valid >= kN : k0 + kN - 1 <= vis_first)) {
                 const int lim = min(valid - 1, ctx ? kN : vis - k0);  // keys [0, lim] visible
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
-                  if (i > lim) sr[i] = 0xFF800000u;                  // -inf
+                  if (i > lim) sr[i] = -INFINITY;
               }
-              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              float mx[4];
 #pragma unroll
-              for (int i = 0; i < 128; i += 4) {
+              for (int e = 0; e < 4; ++e) mx[e] = max3(sr[e], sr[e + 4], sr[e + 8]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sr[i + e]));
-              }
+              for (int i = 12; i < 124; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sr[i + e], sr[i + 4 + e]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sr[124 + e]);
               const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
               const bool raise = mt > m + kRaise || (m == -INFINITY && mt != -INFINITY);
               if (__any_sync(0xffffffffu, raise)) {
                 const float mn = raise ? mt : m;
                 const float alpha = (raise && m != -INFINITY) ? ex2(m - mn) : 1.f;
                 m = mn;
-                l0 *= alpha;
-                l1 *= alpha;
-                if (t > b.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  sum[e].x *= alpha;
+                  sum[e].y *= alpha;
+                }
+                if (t > t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                  if (!two) {  // the previous product may still run (two halves: it cannot)
+                    ok = wait(pdone, (npd + (t - t0) - 1) & 1);
+                    if (!ok) break;
+                    fence_after();
+                  }
 #pragma unroll 1
-                  for (int ch = 0; ch < D / 32; ++ch) {
-                    uint32_t ov[32];
-                    ld32(o_col + ch * 32, ov);
+                  for (int ch = 0; ch < D / 16; ++ch) {
+                    uint32_t ov[16];
+                    ld16(o_col + ch * 16, ov);
                     wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int i = 0; i < 16; ++i)
                       ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-                    st32(o_col + ch * 32, ov);
+                    st16(o_col + ch * 16, ov);
                   }
                 }
               }
               // the probabilities in bf16 over the scores' columns (their sum in fp32)
               const float neg = m == -INFINITY ? 0.f : -m;
+              const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
 #pragma unroll
-              for (int ch = 0; ch < 2; ++ch) {
-                uint32_t pk[32];
+              for (int ch = 0; ch < 8; ++ch) {
+                uint32_t pk[8];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float p0 = ex2(fmaf(__uint_as_float(sr[ch * 64 + 2 * i]), c, neg));
-                  const float p1 = ex2(fmaf(__uint_as_float(sr[ch * 64 + 2 * i + 1]), c, neg));
-                  l0 += p0;
-                  l1 += p1;
-                  pk[i] = pack_bf16(p0, p1);
+                for (int i = 0; i < 8; ++i) {
+                  float2 x = __ffma2_rn(make_float2(sr[ch * 16 + 2 * i], sr[ch * 16 + 2 * i + 1]),
+                                        c2, n2);
+                  x.x = ex2(x.x);
+                  x.y = ex2(x.y);
+                  sum[i & 1] = __fadd2_rn(sum[i & 1], x);
+                  pk[i] = pack_bf16(x.x, x.y);
                 }
-                st32(s_col + ch * 32, pk);
+                st8(s_col + ch * 8, pk);
               }
               wait_st();
             }
             // V rows past the end hold anything: cleared, for 0 * NaN would reach O
             if (h == 0 && valid < kN) {
-              const uint32_t q = seq + 2 * (t - b.t0) + 1;
+              const uint32_t q = seq + 2 * (t - t0) + 1;
               ok = wait(&full[q % NS], (q / NS) & 1);
               if (!ok) break;
               if (lrow >= valid) {
@@ -609,31 +764,34 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               fence_proxy_async_smem();
             }
             fence_before();
-            mbar_arrive(&pfull[h]);
+            mbar_arrive(&pfull[bar]);
           }
+          l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
+        const int n = t1 - t0;
         seq += 2 * n;
+        if (!two) npd += n;
         if (!ok) break;
         // the next block's queries go out while this block's last product runs
         if (more) {
           walk.next(w, lane);
           if (h == 0 || w.rows > kHalf) stage_q(w);
         }
+        const Work& b = blocks[warp - 2];
+        const bool begins = t0 == 0, ends = t1 == b.n_tiles;
         if (active) {
-          ok = wait(&odone[h], nblk & 1);
-          ++nblk;
+          ok = wait(&odone[h], no++ & 1);
           if (!ok) break;
           fence_after();
           const int row = h * kHalf + lrow;
-          const float l = l0 + l1;
           const bool whole = begins && ends;
           const float inv = l > 0.f ? 1.f / l : 0.f;
           const int tok = b.blk * walk.TB + row / Gq;
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.O) +
                                ((int64_t)(b.q.a + tok) * p.h_q + b.head * Gq + row % Gq) * D;
-          const int64_t slot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
-          float* part = p.tc_o + slot * D;
-          if (h * kHalf + (warp & 3) * 32 < b.rows) {
+          const int64_t pslot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
+          float* part = p.tc_o + pslot * D;
+          if (any_row) {
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
               uint32_t ov[32];
@@ -660,16 +818,17 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               }
             }
             if (!whole && row < b.rows)
-              *reinterpret_cast<float2*>(p.tc_ml + slot * 2) = make_float2(m, l);
+              *reinterpret_cast<float2*>(p.tc_ml + pslot * 2) = make_float2(m, l);
           }
           fence_before();  // O is read before the next block's products
         }
-        if (begins && !ends) {  // goes on in the next CTAs' shares
-          const int64_t end = x1 - b.t1 + b.n_tiles - 1;
-          tail = make_int4(b.q.a, b.q.T, b.blk,
-                           (int)(((end + 1) * G + total - 1) / total - 1));
+        if (begins && !ends && tid == 64) {  // goes on in the next CTAs' shares
+          const int64_t end = share.x1 - t1 + b.n_tiles;
+          tail_item = make_int4(b.q.a, b.q.T, b.blk,
+                                (int)((end * share.G + share.total - 1) / share.total - 1));
           tail_head = b.head;
         }
+        __syncwarp();  // the block is read before the next one takes its place
         if (!more) break;
       }
     }
@@ -682,9 +841,9 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   }
   if (err) atomicCAS(&cta_err, 0, err);
   __syncthreads();
-  if (tid == 64) {  // the first softmax thread knows the share's last block
-    if (cta_err == kErrWaitTimeout) tail.x = -1;
-    p.tc_tail[2 * blockIdx.x] = tail;
+  if (tid == 0) {
+    if (cta_err == kErrWaitTimeout) tail_item.x = -1;
+    p.tc_tail[2 * blockIdx.x] = tail_item;
     p.tc_tail[2 * blockIdx.x + 1] = make_int4(tail_head, 0, 0, 0);
     p.err_cta[p.tc_err_at + blockIdx.x] = cta_err;
   }

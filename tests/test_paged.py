@@ -537,6 +537,11 @@ ATTEND = {
     "prompts": ([130, 1, 257, 64], [130, 1, 257, 64], 16, 4, 1, 64, None),
     "mixed": ([700, 33, 400, 1, 129], [1, 33, 100, 1, 60], 32, 16, 4, 128, [8, 0, 40, 3, 1]),
     "big_page": ([1000, 5], [1, 2], 1024, 4, 2, 128, None),
+    # blocks of one half and of two follow one another within a CTA's share
+    "halves_alternate": ([900 + 37 * i for i in range(24)], [6 if i % 2 else 45 for i in range(24)],
+                         64, 32, 8, 128, [i % 5 * 8 for i in range(24)]),
+    "halves_alternate_d64": ([700 + 61 * i for i in range(20)],
+                             [(3, 70, 5, 40)[i % 4] for i in range(20)], 16, 32, 4, 64, None),
     "many_kv_heads": ([40, 9], [2, 1], 16, 24, 12, 64, [3, 0]),
 }
 
