@@ -204,11 +204,11 @@ struct Walk {
         sum = (int64_t)full * (ct + x / kN) + (int64_t)(TB / kN) * full * (full - 1) / 2;
         b = full;
       } else if (kN % TB == 0) {
-        // with x = 128 e + TB u + v, v < TB, block b has e + floor((u + b) / (128 / TB))
-        const int per = kN / TB, u = x % kN / TB;
-        const int64_t end = u + full, whole = end / per;  // sum of floor(i / per), u <= i < end
-        sum = (int64_t)full * (ct + x / kN) + per * (whole * (whole - 1) / 2) +
-              whole * (end - whole * per);
+        // with x = 128 e + TB u + v, v < TB, block b has e + floor((u + b) / per), per = 128 / TB
+        const int lg = __ffs(kN / TB) - 1, u = (x % kN) >> (7 - lg);  // per = 2^lg
+        const int end = u + full, whole = end >> lg;  // sum of floor(i / per), u <= i < end
+        sum = (int64_t)full * (ct + x / kN) + (((int64_t)whole * (whole - 1) / 2) << lg) +
+              (int64_t)whole * (end - (whole << lg));
         b = full;
       }
     }
@@ -236,9 +236,11 @@ struct Walk {
   __device__ __forceinline__ void first(Work& w, int r, int64_t off) {
     enter(w, r);
     const int64_t per_head = request_tiles(w.q);
-    w.head = (int)(off / per_head);
-    const int64_t rem = off % per_head;
+    const bool small = ((off | per_head) >> 32) == 0;  // a 64-bit division is ten times a 32-bit one
+    w.head = small ? (int)((uint32_t)off / (uint32_t)per_head) : (int)(off / per_head);
+    const int64_t rem = off - w.head * per_head;
     int lo = 0, hi = w.nb;  // first_blocks(lo) <= rem < first_blocks(hi)
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (first_blocks(w.q, mid) <= rem) lo = mid;
@@ -338,6 +340,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   int err = 0;
   int64_t total = 0, mine = 0;
   int G = 1;  // shares: no more than tiles, so that none of them is empty
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const int64_t x0 = pass ? total * blockIdx.x / G : 0;
     int64_t carry = 0;
@@ -433,8 +436,9 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           for (int kv = 0; kv < 2; ++kv, ++seq) {
             const int s = seq % NS;
             if (seq >= NS) {
-              ok = wait_or_abort(&empty[s], ((seq / NS) - 1) & 1, &cta_err, abort_flag);
-              ok = __all_sync(0xffffffffu, ok);
+              if (lane == 0)
+                ok = wait_or_abort(&empty[s], ((seq / NS) - 1) & 1, &cta_err, abort_flag);
+              ok = uniform(ok) != 0;
               if (!ok) break;
             }
             if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
@@ -584,65 +588,68 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       auto wait = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, par, &cta_err, abort_flag));
       };
-      // The warp's 32 query rows, rotated, rounded to bf16 and staged as the K-major operand.
-      // A lane takes the RoPE pairs 2l, 2l + 1 of a row (D = 64: of one of two rows), so a
-      // token's angles are computed once for the rows of its heads that follow one another.
+      // The warp's 32 query rows, rotated, rounded to bf16 and staged as the K-major operand
+      // (element e of row r in slice e / 64 at 16-byte chunk (e % 64) / 8 ^ (r & 7)): copied
+      // as they are, then turned in place, a lane the RoPE pairs 2l, 2l + 1 of a row (D = 64: of
+      // one of two rows). The angles of the first token are exact, the next ones follow by
+      // rotating on: at most 32 steps of 2^-23, against 2^-9 of the rounding to bf16. The loops
+      // are not unrolled: this code is cold at a block's start, and its instruction fetches took
+      // 9 us a block when it was.
       auto stage_q = [&](const Work& b) {
-        constexpr int LPR = D / 4;             // lanes a row takes
-        constexpr int RPS = 32 / LPR;          // rows at once
-        const int l = lane % LPR;
-        int64_t pos0 = (int64_t)p.pos0 + b.q.L - b.q.T;
-        const unsigned long long F0 = p.rope_turns[2 * l], F1 = p.rope_turns[2 * l + 1];
         const int row0 = h * kHalf + (warp & 3) * 32;          // the warp's first row
-        if (row0 < b.rows) {
-          int g = (row0 + lane / LPR) % Gq;                    // the lane's row, step by step
-          int tok = (row0 + lane / LPR) / Gq;
-          const int last_tok = (b.rows - 1) / Gq;              // rows past the block's repeat a
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) +  // row of its last
-                                     (int64_t)(b.q.a + b.blk * walk.TB) * p.q_stride +  // token
+        const int n_row = min(32, b.rows - row0);
+        if (n_row > 0) {
+          unsigned char* rows = q_s + h * C::kTile + (warp & 3) * 32 * 128;
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) +
+                                     (int64_t)(b.q.a + b.blk * walk.TB) * p.q_stride +
                                      b.head * Gq * D;
-          constexpr int NI = 32 / RPS;
-          uint32_t lo[NI], hi[NI];
-          int tk = min(tok, last_tok), gk = g;
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const uint32_t* at =
-                reinterpret_cast<const uint32_t*>(src + (int64_t)tk * p.q_stride + gk * D);
-            lo[i] = __ldg(at + l);
-            hi[i] = __ldg(at + D / 4 + l);
-            gk += RPS;
-            while (gk >= Gq) {
-              gk -= Gq;
-              tk = min(tk + 1, last_tok);
+          constexpr int CPR = D / 8;                           // 16-byte chunks of a row
+          {
+            const int ch = lane % CPR;
+            int r = lane / CPR, tok = (row0 + r) / Gq, g = (row0 + r) % Gq;
+#pragma unroll 1
+            for (; r < n_row; r += 32 / CPR) {
+              cp_async16_cg(rows + (ch >> 3) * kSlice + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                            src + (int64_t)tok * p.q_stride + g * D + ch * 8);
+              for (g += 32 / CPR; g >= Gq; g -= Gq) ++tok;
             }
           }
-          pos0 += b.blk * walk.TB;
-          int have = -1;
-          float2 c0 = make_float2(1.f, 0.f), c1 = c0;
-          unsigned char* row = q_s + h * C::kTile + ((warp & 3) * 32 + lane / LPR) * 128;
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            if (p.rope && tok != have) {
-              have = tok;
-              c0 = rot_turns(pos0 + tok, F0);
-              c1 = rot_turns(pos0 + tok, F1);
+          constexpr int LPR = D / 4;                           // lanes that turn a row
+          const int l = lane % LPR;
+          int r = lane / LPR, tok = (row0 + r) / Gq, g = (row0 + r) % Gq;
+          float2 c0 = make_float2(1.f, 0.f), c1 = c0, s0 = c0, s1 = c0;
+          if (p.rope) {
+            const int64_t pos = (int64_t)p.pos0 + b.q.L - b.q.T + b.blk * walk.TB + tok;
+            const unsigned long long F0 = p.rope_turns[2 * l], F1 = p.rope_turns[2 * l + 1];
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              const float2 a = rot_turns(i ? 1 : pos, F0), c = rot_turns(i ? 1 : pos, F1);
+              if (i) {
+                s0 = a;
+                s1 = c;
+              } else {
+                c0 = a;
+                c1 = c;
+              }
             }
-            const float a0 = __uint_as_float(lo[i] << 16), a1 = __uint_as_float(lo[i] & 0xFFFF0000u);
-            const float b0 = __uint_as_float(hi[i] << 16), b1 = __uint_as_float(hi[i] & 0xFFFF0000u);
-            const uint32_t ra = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-            const uint32_t rb = pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
-            // element e of row r: slice e / 64, 16-byte chunk (e % 64) / 8 ^ (r & 7)
-            unsigned char* dst = row + i * RPS * 128;
-            const int x = (lane / LPR + i * RPS) & 7;
-            const int ea = 2 * l, eb = 2 * l + D / 2;
-            *reinterpret_cast<uint32_t*>(dst + (ea >> 6) * kSlice + ((((ea & 63) >> 3) ^ x) << 4) +
-                                         (ea & 7) * 2) = ra;
-            *reinterpret_cast<uint32_t*>(dst + (eb >> 6) * kSlice + ((((eb & 63) >> 3) ^ x) << 4) +
-                                         (eb & 7) * 2) = rb;
-            g += RPS;
-            while (g >= Gq) {
-              g -= Gq;
-              ++tok;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+          const int ea = 2 * l, eb = 2 * l + D / 2;
+          unsigned char* pa = rows + (ea >> 6) * kSlice + (ea & 7) * 2;
+          unsigned char* pb = rows + (eb >> 6) * kSlice + (eb & 7) * 2;
+#pragma unroll 2
+          for (; r < n_row; r += 32 / LPR) {
+            uint32_t* wa = reinterpret_cast<uint32_t*>(pa + r * 128 + ((((ea & 63) >> 3) ^ (r & 7)) << 4));
+            uint32_t* wb = reinterpret_cast<uint32_t*>(pb + r * 128 + ((((eb & 63) >> 3) ^ (r & 7)) << 4));
+            const uint32_t lo = *wa, hi = *wb;
+            const float a0 = __uint_as_float(lo << 16), a1 = __uint_as_float(lo & 0xFFFF0000u);
+            const float b0 = __uint_as_float(hi << 16), b1 = __uint_as_float(hi & 0xFFFF0000u);
+            *wa = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+            *wb = pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
+            for (g += 32 / LPR; g >= Gq; g -= Gq) {
+              c0 = make_float2(c0.x * s0.x - c0.y * s0.y, c0.y * s0.x + c0.x * s0.y);
+              c1 = make_float2(c1.x * s1.x - c1.y * s1.y, c1.y * s1.x + c1.x * s1.y);
             }
           }
         }
@@ -792,7 +799,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           const int64_t pslot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
           float* part = p.tc_o + pslot * D;
           if (any_row) {
-#pragma unroll
+#pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
               uint32_t ov[32];
               ld32(o_col + ch * 32, ov);
