@@ -265,6 +265,7 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
   p.tc_tail = reinterpret_cast<int4*>(take(pl.tc_tail_bytes));
   p.tc_ml = reinterpret_cast<float*>(take(pl.tc_ml_bytes));
   p.tc_o = reinterpret_cast<float*>(take(pl.tc_o_bytes));
+  p.q_rot = reinterpret_cast<__nv_bfloat16*>(take(pl.q_bytes));
   p.tc_rows = pl.tc_grid > 0 ? msa::kPagedWarpRows : INT32_MAX;
   p.tc_err_at = pl.grid;
   return done(msa::launch_paged_attend(p, pl, dtype, d, st), "msa_paged_attend launch");

@@ -389,13 +389,16 @@ struct PagedAttendParams {
   int4* tc_tail;            // [tc_grid][2]
   float* tc_ml;             // [tc_grid][2][256][2] its partials
   float* tc_o;              // [tc_grid][2][256][d]
+  __nv_bfloat16* q_rot;     // [h_kv][d / 64][n_rows * h_q / h_kv][64] its rotated queries
 };
 struct PagedPlan {
   int grid, S;              // CTAs; ranges that the tile list is cut into (per KV head)
   int tc_grid;              // CTAs of the tcgen05 kernel (0: not launched)
-  size_t err_bytes, tail_bytes, ml_bytes, o_bytes, tc_tail_bytes, tc_ml_bytes, tc_o_bytes, smem;
+  size_t err_bytes, tail_bytes, ml_bytes, o_bytes, tc_tail_bytes, tc_ml_bytes, tc_o_bytes,
+      q_bytes, smem;
   size_t bytes() const {
-    return err_bytes + tail_bytes + ml_bytes + o_bytes + tc_tail_bytes + tc_ml_bytes + tc_o_bytes;
+    return err_bytes + tail_bytes + ml_bytes + o_bytes + tc_tail_bytes + tc_ml_bytes + tc_o_bytes +
+           q_bytes;
   }
 };
 PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int dtype, int sms);

@@ -112,6 +112,68 @@ __device__ __forceinline__ int range_of(int64_t y, int64_t x, int S) {
   return (int)(((y + 1) * S + x - 1) / x - 1);
 }
 
+// The queries of the requests that the tcgen05 kernel serves, rotated and rounded to bf16, in
+// its operand layout: per KV head and 64 dims the rows (token, query head of the group) one after
+// another, 16-byte chunk c of a row at c ^ (row within its block & 7). A warp takes a token: lane =
+// one 16-byte chunk of the lower half of a head and its partner half a head on.
+template <int D>
+__device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w, int n_warps,
+                                               int lane) {
+  constexpr int HC = D / 16;       // chunks of half a head
+  constexpr int HPW = 32 / HC;     // heads a warp takes at once
+  const int Gq = p.h_q / p.h_kv, TB = 256 / Gq;
+  const int c = lane % HC;
+  unsigned long long F[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) F[e] = p.rope_turns[c * 8 + e];
+  const int64_t rows = (int64_t)p.n_rows * Gq;
+  for (int i = w; i < p.n_rows; i += n_warps) {
+    int lo = 0, hi = p.n_req;      // the request of token i: row_start[lo] <= i < row_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.row_start + mid) <= i) lo = mid;
+      else hi = mid;
+    }
+    int ignore = 0;
+    const PagedReq q = paged_req(p, lo, p.tc_rows, INT_MAX, &ignore);
+    const int t = i - q.a;
+    if (t < 0 || t >= q.T) continue;
+    const int64_t pos = (int64_t)p.pos0 + q.L - q.T + t;
+    float2 cs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = p.rope ? rot_turns(pos, F[e]) : make_float2(1.f, 0.f);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + i * p.q_stride;
+#pragma unroll 2
+    for (int h = lane / HC; h < p.h_q; h += HPW) {
+      using V = Vec<__nv_bfloat16, 8>;
+      const uint4 ra = __ldg(reinterpret_cast<const uint4*>(src + h * D + c * 8));
+      const uint4 rb = __ldg(reinterpret_cast<const uint4*>(src + h * D + c * 8 + D / 2));
+      float a[8], b[8];
+      V::unpack(ra, a);
+      V::unpack(rb, b);
+      uint32_t oa[4], ob[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
+        oa[e] = pack_bf16(a[2 * e] * c0.x - b[2 * e] * c0.y,
+                          a[2 * e + 1] * c1.x - b[2 * e + 1] * c1.y);
+        ob[e] = pack_bf16(b[2 * e] * c0.x + a[2 * e] * c0.y,
+                          b[2 * e + 1] * c1.x + a[2 * e + 1] * c1.y);
+      }
+      const int kv = h / Gq, g = h % Gq;
+      const int x = ((t % TB) * Gq + g) & 7;
+      const int64_t row = (int64_t)i * Gq + g;
+      auto put = [&](int chunk, const uint32_t (&v)[4]) {  // chunk of the head's row
+        __nv_bfloat16* dst = p.q_rot + (((int64_t)kv * (D / 64) + chunk / 8) * rows + row) * 64 +
+                             (((chunk & 7) ^ x) << 3);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+      };
+      put(c, oa);
+      put(c + HC, ob);
+    }
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendParams p, int S_max) {
   using G = Geo<T, D>;
@@ -496,6 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     cp_wait<0>();
   }
   if (head == 0 && lane == 0 && s < S_max) p.tail[s] = tail;
+  if constexpr (BF)
+    if (p.tc_rows != INT_MAX) rotate_queries<D>(p, w_all, gridDim.x * kWarps, lane);
   if (err) cta_err = err;
   __syncthreads();
   if (tid == 0) p.err_cta[blockIdx.x] = cta_err;
@@ -693,6 +757,7 @@ PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int
   pl.tc_tail_bytes = al((size_t)pl.tc_grid * 2 * sizeof(int4));
   pl.tc_ml_bytes = al((size_t)pl.tc_grid * 2 * 256 * 2 * sizeof(float));
   pl.tc_o_bytes = al((size_t)pl.tc_grid * 2 * 256 * d * sizeof(float));
+  pl.q_bytes = tc ? al((size_t)n_rows * h_q * d * 2) : 0;
   pl.smem = pga::kWarps * pga::kRing + ((size_t)n_req + 1) * sizeof(int64_t);
   return pl;
 }

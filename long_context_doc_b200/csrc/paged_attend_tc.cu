@@ -8,13 +8,13 @@
 // own scores and accumulator in TMEM, worked on in alternation: while one half's softmax runs,
 // the tensor cores form the other half's products, and both halves use every K and V tile that
 // was loaded. Warp 0 copies the tiles (one TMA box of 64 dims per page and half a head) into a
-// ring of K and V tiles; one thread of warp 1 issues tcgen05.mma: S = Q K^T, then O += P V with P
+// ring of K and V tiles, and a block's queries, which the warp-level kernel has rotated, rounded to
+// bf16 and laid out as the operand wants them; one thread of warp 1 issues tcgen05.mma: S = Q K^T, then O += P V with P
 // read from TMEM, where the softmax put it over the scores, and V as an MN-major operand as
-// stored. Warps 2-9 hold one query row per thread: they rotate and stage their half's queries,
-// load the 128 scores of a tile from TMEM once, mask, and keep the running maximum (raised, with
+// stored. Warps 2-9 hold one query row per thread: they load the 128 scores of a tile from TMEM once, mask, and keep the running maximum (raised, with
 // O rescaled in TMEM, only when a tile's maximum passes it by more than 8 in log2 units) and sum
 // in fp32. With two halves a half's completed scores imply its earlier products (the issuing
-// thread's MMAs complete in order), so O is rescaled and Q replaced without further waits. A
+// thread's MMAs complete in order), so O is rescaled without further waits. A
 // block of one half has both scores buffers to itself: the scores of a tile are formed before
 // the product of the tile before it.
 // Every wait is bounded; on expiry the CTA records kErrWaitTimeout, lets its copies and MMAs
@@ -34,13 +34,14 @@ constexpr int kN = 128;                   // keys of a tile
 constexpr int kHalf = 128;                // query rows of a half
 constexpr int kThreads = 320;
 constexpr uint32_t kSlice = 128 * 128;    // 128 rows x 64 bf16, 128-byte swizzle: 16 KB
+constexpr uint32_t kBounce = 32 * 128;    // a warp's 128 bytes of 32 rows on their way to memory
 constexpr float kRaise = 8.f;
 
 template <int D> struct Cfg {
   static constexpr int SL = D / 64;                    // slices of a tile
   static constexpr uint32_t kTile = SL * kSlice;       // K or V tile, and one half's Q
-  static constexpr int NS = D == 128 ? 5 : 8;          // ring tiles
-  static constexpr size_t smem = 1024 + 2 * kTile + NS * kTile + 512;
+  static constexpr int NS = D == 128 ? 4 : 8;          // ring tiles (5 measured the same)
+  static constexpr size_t smem = 1024 + 2 * kTile + NS * kTile + 8 * kBounce + 512;
 };
 
 __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -285,17 +286,19 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   unsigned char* base = smem_align1024(sm_raw);
   unsigned char* q_s = base;                       // [2 halves][SL][128][64]
   unsigned char* ring = base + 2 * C::kTile;       // [NS][SL][128][64]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + NS * C::kTile);
+  unsigned char* bounce = ring + NS * C::kTile;    // [8 warps][32 rows][128 bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bounce + 8 * kBounce);
   uint64_t* full = bars;            // [NS] ring tile landed
   uint64_t* empty = bars + NS;      // [NS] ring tile consumed
   // (each with one waiting party that sees every phase: entry 2 is half 0's, for the tiles of a
   // one-half block that use the second scores buffer)
-  uint64_t* qfull = bars + 2 * NS;  // [2] a half's queries staged (128 threads)
+  uint64_t* qfull = bars + 2 * NS;  // [2] a half's queries landed
   uint64_t* sfull = qfull + 2;      // [3] scores written
   uint64_t* pfull = qfull + 5;      // [3] probabilities written (128 threads)
   uint64_t* odone = qfull + 8;      // [2] a block's last P V of the half completed
   uint64_t* pdone = qfull + 10;     // a P V of a one-half block completed
-  uint64_t* done = qfull + 11;      // every issued MMA completed
+  uint64_t* qempty = qfull + 11;    // [2] a block's last scores of the half formed
+  uint64_t* done = qfull + 13;      // every issued MMA completed
   __shared__ int64_t warp_tot[kThreads / 32];
   __shared__ int64_t start_off;
   __shared__ int start_r, cta_err;
@@ -317,7 +320,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       mbar_init(&empty[s], 1);
     }
     for (int h = 0; h < 2; ++h) {
-      mbar_init(&qfull[h], kHalf);
+      mbar_init(&qfull[h], 1);
+      mbar_init(&qempty[h], 1);
       mbar_init(&odone[h], 1);
     }
     for (int i = 0; i < 3; ++i) {
@@ -406,7 +410,30 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       const int br = min(ps, kN);               // rows of a box
       const int half = lane % SL, piece = lane / SL;
       bool ok = true;
+      uint32_t nq[2] = {0, 0};
+      // the rotated queries are written by the grid launched before this one
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       while (ok) {
+        // the block's queries: a half's rows are consecutive in each slice of its head's
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int rows = min(w.rows - h * kHalf, kHalf);
+          if (rows <= 0) continue;
+          if (lane == 0 && nq[h] > 0)
+            ok = ok && wait_or_abort(&qempty[h], (nq[h] - 1) & 1, &cta_err, abort_flag);
+          ok = uniform(ok) != 0;
+          if (!ok) break;
+          ++nq[h];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&qfull[h], (uint32_t)(rows * 128 * SL));
+            for (int sl = 0; sl < SL; ++sl)
+              bulk_g2s(q_s + h * C::kTile + sl * kSlice,
+                       p.q_rot + (((int64_t)w.head * SL + sl) * p.n_rows * Gq +
+                                  (int64_t)(w.q.a + w.blk * walk.TB) * Gq + h * kHalf) * 64,
+                       (uint32_t)rows * 128u, &qfull[h]);
+          }
+          __syncwarp();
+        }
         for (int t = w.t0; ok && t < w.t1; ++t) {
           const bool ctx = t < w.CT;
           const int k0 = (ctx ? t : t - w.CT) * kN;
@@ -454,6 +481,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         walk.next(w, lane);
       }
       // the copies issued land before the CTA can exit
+      for (int h = 0; h < 2; ++h)
+        if (nq[h] > 0) mbar_wait_bounded(&qfull[h], (nq[h] - 1) & 1, &cta_err);
       for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
         mbar_wait_bounded(&full[q % NS], (q / NS) & 1, &cta_err);
     } else if (warp == 1) {
@@ -506,6 +535,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             ok = ok && wait(&qfull[h], nq[h] & 1);
             ++nq[h];
             if (ok) scores(h, h, h, rs);
+            if (ok && n == 1) commit(&qempty[h]);
           }
           if (!ok) break;
           commit(&empty[rs]);
@@ -525,6 +555,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               ok = wait_ring();
               if (!ok) break;
               scores(0, 0, 0, rs);
+              if (j + 2 == n) commit(&qempty[0]);
             }
             ok = wait(&pfull[1], np[1] & 1);
             ++np[1];
@@ -535,6 +566,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               commit(&odone[1]);
             } else {
               scores(1, 1, 1, rs);
+              if (j + 2 == n) commit(&qempty[1]);
               commit(&empty[rs]);
               advance();
             }
@@ -545,6 +577,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           ++nq[0];
           if (!ok) break;
           scores(0, 0, 0, rs);
+          if (n == 1) commit(&qempty[0]);
           commit(&empty[rs]);
           advance();
 #pragma unroll 1
@@ -557,6 +590,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               ok = wait_ring();
               if (!ok) break;
               scores(0, slot ^ 1, slot ? 0 : 2, rs);
+              if (j + 2 == n) commit(&qempty[0]);
               commit(&empty[rs]);
               advance();
             }
@@ -588,76 +622,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       auto wait = [&](uint64_t* bar, uint32_t par) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, par, &cta_err, abort_flag));
       };
-      // The warp's 32 query rows, rotated, rounded to bf16 and staged as the K-major operand
-      // (element e of row r in slice e / 64 at 16-byte chunk (e % 64) / 8 ^ (r & 7)): copied
-      // as they are, then turned in place, a lane the RoPE pairs 2l, 2l + 1 of a row (D = 64: of
-      // one of two rows). The angles of the first token are exact, the next ones follow by
-      // rotating on: at most 32 steps of 2^-23, against 2^-9 of the rounding to bf16. The loops
-      // are not unrolled: this code is cold at a block's start, and its instruction fetches took
-      // 9 us a block when it was.
-      auto stage_q = [&](const Work& b) {
-        const int row0 = h * kHalf + (warp & 3) * 32;          // the warp's first row
-        const int n_row = min(32, b.rows - row0);
-        if (n_row > 0) {
-          unsigned char* rows = q_s + h * C::kTile + (warp & 3) * 32 * 128;
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) +
-                                     (int64_t)(b.q.a + b.blk * walk.TB) * p.q_stride +
-                                     b.head * Gq * D;
-          constexpr int CPR = D / 8;                           // 16-byte chunks of a row
-          {
-            const int ch = lane % CPR;
-            int r = lane / CPR, tok = (row0 + r) / Gq, g = (row0 + r) % Gq;
-#pragma unroll 1
-            for (; r < n_row; r += 32 / CPR) {
-              cp_async16_cg(rows + (ch >> 3) * kSlice + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                            src + (int64_t)tok * p.q_stride + g * D + ch * 8);
-              for (g += 32 / CPR; g >= Gq; g -= Gq) ++tok;
-            }
-          }
-          constexpr int LPR = D / 4;                           // lanes that turn a row
-          const int l = lane % LPR;
-          int r = lane / LPR, tok = (row0 + r) / Gq, g = (row0 + r) % Gq;
-          float2 c0 = make_float2(1.f, 0.f), c1 = c0, s0 = c0, s1 = c0;
-          if (p.rope) {
-            const int64_t pos = (int64_t)p.pos0 + b.q.L - b.q.T + b.blk * walk.TB + tok;
-            const unsigned long long F0 = p.rope_turns[2 * l], F1 = p.rope_turns[2 * l + 1];
-#pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-              const float2 a = rot_turns(i ? 1 : pos, F0), c = rot_turns(i ? 1 : pos, F1);
-              if (i) {
-                s0 = a;
-                s1 = c;
-              } else {
-                c0 = a;
-                c1 = c;
-              }
-            }
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          __syncwarp();
-          const int ea = 2 * l, eb = 2 * l + D / 2;
-          unsigned char* pa = rows + (ea >> 6) * kSlice + (ea & 7) * 2;
-          unsigned char* pb = rows + (eb >> 6) * kSlice + (eb & 7) * 2;
-#pragma unroll 2
-          for (; r < n_row; r += 32 / LPR) {
-            uint32_t* wa = reinterpret_cast<uint32_t*>(pa + r * 128 + ((((ea & 63) >> 3) ^ (r & 7)) << 4));
-            uint32_t* wb = reinterpret_cast<uint32_t*>(pb + r * 128 + ((((eb & 63) >> 3) ^ (r & 7)) << 4));
-            const uint32_t lo = *wa, hi = *wb;
-            const float a0 = __uint_as_float(lo << 16), a1 = __uint_as_float(lo & 0xFFFF0000u);
-            const float b0 = __uint_as_float(hi << 16), b1 = __uint_as_float(hi & 0xFFFF0000u);
-            *wa = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-            *wb = pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
-            for (g += 32 / LPR; g >= Gq; g -= Gq) {
-              c0 = make_float2(c0.x * s0.x - c0.y * s0.y, c0.y * s0.x + c0.x * s0.y);
-              c1 = make_float2(c1.x * s1.x - c1.y * s1.y, c1.y * s1.x + c1.x * s1.y);
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&qfull[h]);
-      };
       bool ok = true;
-      if (h == 0 || w.rows > kHalf) stage_q(w);
       while (true) {
         // The block's geometry is kept in shared memory for its end and the walk: the tile loop
         // holds a row of scores in registers.
@@ -779,11 +744,6 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         seq += 2 * n;
         if (!two) npd += n;
         if (!ok) break;
-        // the next block's queries go out while this block's last product runs
-        if (more) {
-          walk.next(w, lane);
-          if (h == 0 || w.rows > kHalf) stage_q(w);
-        }
         const Work& b = blocks[warp - 2];
         const bool begins = t0 == 0, ends = t1 == b.n_tiles;
         if (active) {
@@ -792,39 +752,56 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           fence_after();
           const int row = h * kHalf + lrow;
           const bool whole = begins && ends;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          const int tok = b.blk * walk.TB + row / Gq;
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.O) +
-                               ((int64_t)(b.q.a + tok) * p.h_q + b.head * Gq + row % Gq) * D;
-          const int64_t pslot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
-          float* part = p.tc_o + pslot * D;
+          // A lane holds a row: its 128-byte pieces go through shared memory (16-byte chunk c of
+          // row r at c ^ (r & 7)), so that eight lanes write a piece of one row together.
           if (any_row) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int64_t pslot =
+                ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
+            const int tok = b.blk * walk.TB + row / Gq;
+            unsigned char* dst =
+                whole ? reinterpret_cast<unsigned char*>(
+                            static_cast<__nv_bfloat16*>(p.O) +
+                            ((int64_t)(b.q.a + tok) * p.h_q + b.head * Gq + row % Gq) * D)
+                      : reinterpret_cast<unsigned char*>(p.tc_o + pslot * D);
+            unsigned char* mine = bounce + (warp - 2) * kBounce;
+            const int n_row = b.rows - (row - lane);             // the warp's rows
+            const int steps = whole ? D / 64 : D / 32;
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
+            for (int st = 0; st < steps; ++st) {
               uint32_t ov[32];
-              ld32(o_col + ch * 32, ov);
-              wait_ld();
-              if (row < b.rows) {
-                if (whole) {
+              if (whole) {
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    uint32_t v[4];
+                for (int hf = 0; hf < 2; ++hf) {
+                  uint32_t f[32];
+                  ld32(o_col + st * 64 + hf * 32, f);
+                  wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      v[e] = pack_bf16(__uint_as_float(ov[8 * i + 2 * e]) * inv,
-                                       __uint_as_float(ov[8 * i + 2 * e + 1]) * inv);
-                    *reinterpret_cast<uint4*>(out + ch * 32 + 8 * i) =
-                        make_uint4(v[0], v[1], v[2], v[3]);
-                  }
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(part + ch * 32 + 4 * i) =
-                        make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+                  for (int i = 0; i < 16; ++i)
+                    ov[hf * 16 + i] = pack_bf16(__uint_as_float(f[2 * i]) * inv,
+                                                __uint_as_float(f[2 * i + 1]) * inv);
                 }
+              } else {
+                ld32(o_col + st * 32, ov);
+                wait_ld();
               }
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(mine + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                    make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3);
+                unsigned char* to = reinterpret_cast<unsigned char*>(__shfl_sync(
+                    0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+                const uint4 v = *reinterpret_cast<const uint4*>(mine + r * 128 +
+                                                                (((lane & 7) ^ (r & 7)) << 4));
+                if (r < n_row) *reinterpret_cast<uint4*>(to + st * 128 + (lane & 7) * 16) = v;
+              }
+              __syncwarp();
             }
-            if (!whole && row < b.rows)
+            if (!whole && lane < n_row)
               *reinterpret_cast<float2*>(p.tc_ml + pslot * 2) = make_float2(m, l);
           }
           fence_before();  // O is read before the next block's products
@@ -837,6 +814,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         }
         __syncwarp();  // the block is read before the next one takes its place
         if (!more) break;
+        walk.next(w, lane);
       }
     }
     fence_before();
