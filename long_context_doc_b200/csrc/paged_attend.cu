@@ -31,8 +31,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = kPagedWarpRows;  // query rows of a block (the MMA's M)
 constexpr int kRing = 24576;        // bytes of a warp's ring
-constexpr int kMinTiles = 4;        // a range is at least this many tiles
-constexpr int kMergeThreads = 256;
+constexpr int kMinTiles = 2;        // a range is at least this many tiles
+constexpr int kAngles = 2048;       // bytes of a warp's angle table: the tokens of a query block
+constexpr int kMergeThreads = 512;
 
 template <typename T, int D> struct Geo {
   static constexpr int KT = sizeof(T) == 2 ? 16 : 8;      // keys of a tile
@@ -114,19 +115,17 @@ __device__ __forceinline__ int range_of(int64_t y, int64_t x, int S) {
 
 // The queries of the requests that the tcgen05 kernel serves, rotated and rounded to bf16, in
 // its operand layout: per KV head and 64 dims the rows (token, query head of the group) one after
-// another, 16-byte chunk c of a row at c ^ (row within its block & 7). A warp takes a token: lane =
-// one 16-byte chunk of the lower half of a head and its partner half a head on.
+// another, 16-byte chunk c of a row at c ^ (row within its block & 7). A warp takes a token, a
+// lane the RoPE pairs 2l, 2l + 1 of each of its heads (D = 64: of every other head).
 template <int D>
 __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w, int n_warps,
                                                int lane) {
-  constexpr int HC = D / 16;       // chunks of half a head
-  constexpr int HPW = 32 / HC;     // heads a warp takes at once
+  constexpr int LPH = D / 4;       // lanes of a head
+  constexpr int HPW = 32 / LPH;    // heads a warp takes at once
   const int Gq = p.h_q / p.h_kv, TB = 256 / Gq;
-  const int c = lane % HC;
-  unsigned long long F[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) F[e] = p.rope_turns[c * 8 + e];
+  const int l = lane % LPH;
   const int64_t rows = (int64_t)p.n_rows * Gq;
+#pragma unroll 1
   for (int i = w; i < p.n_rows; i += n_warps) {
     int lo = 0, hi = p.n_req;      // the request of token i: row_start[lo] <= i < row_start[hi]
     while (hi - lo > 1) {
@@ -139,37 +138,30 @@ __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w
     const int t = i - q.a;
     if (t < 0 || t >= q.T) continue;
     const int64_t pos = (int64_t)p.pos0 + q.L - q.T + t;
-    float2 cs[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = p.rope ? rot_turns(pos, F[e]) : make_float2(1.f, 0.f);
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + i * p.q_stride;
-#pragma unroll 2
-    for (int h = lane / HC; h < p.h_q; h += HPW) {
-      using V = Vec<__nv_bfloat16, 8>;
-      const uint4 ra = __ldg(reinterpret_cast<const uint4*>(src + h * D + c * 8));
-      const uint4 rb = __ldg(reinterpret_cast<const uint4*>(src + h * D + c * 8 + D / 2));
-      float a[8], b[8];
-      V::unpack(ra, a);
-      V::unpack(rb, b);
-      uint32_t oa[4], ob[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
-        oa[e] = pack_bf16(a[2 * e] * c0.x - b[2 * e] * c0.y,
-                          a[2 * e + 1] * c1.x - b[2 * e + 1] * c1.y);
-        ob[e] = pack_bf16(b[2 * e] * c0.x + a[2 * e] * c0.y,
-                          b[2 * e + 1] * c1.x + a[2 * e + 1] * c1.y);
-      }
-      const int kv = h / Gq, g = h % Gq;
-      const int x = ((t % TB) * Gq + g) & 7;
-      const int64_t row = (int64_t)i * Gq + g;
-      auto put = [&](int chunk, const uint32_t (&v)[4]) {  // chunk of the head's row
-        __nv_bfloat16* dst = p.q_rot + (((int64_t)kv * (D / 64) + chunk / 8) * rows + row) * 64 +
-                             (((chunk & 7) ^ x) << 3);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+    float2 c0 = make_float2(1.f, 0.f), c1 = c0;
+    if (p.rope) {
+      c0 = rot_turns(pos, p.rope_turns[2 * l]);
+      c1 = rot_turns(pos, p.rope_turns[2 * l + 1]);
+    }
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        static_cast<const __nv_bfloat16*>(p.Q) + i * p.q_stride);
+    int h = lane / LPH, kv = h / Gq, g = h % Gq;
+    const int x0 = (t % TB) * Gq;
+#pragma unroll 4
+    for (; h < p.h_q; h += HPW) {
+      const uint32_t lo2 = __ldg(src + h * (D / 2) + l), hi2 = __ldg(src + h * (D / 2) + D / 4 + l);
+      const float a0 = __uint_as_float(lo2 << 16), a1 = __uint_as_float(lo2 & 0xFFFF0000u);
+      const float b0 = __uint_as_float(hi2 << 16), b1 = __uint_as_float(hi2 & 0xFFFF0000u);
+      const int x = (x0 + g) & 7;
+      // element e of a head: 64 dims e / 64, chunk (e % 64) / 8
+      auto put = [&](int e, uint32_t v) {
+        unsigned char* row = reinterpret_cast<unsigned char*>(
+            p.q_rot + (((int64_t)kv * (D / 64) + (e >> 6)) * rows + (int64_t)i * Gq + g) * 64);
+        *reinterpret_cast<uint32_t*>(row + ((((e & 63) >> 3) ^ x) << 4) + (e & 7) * 2) = v;
       };
-      put(c, oa);
-      put(c + HC, ob);
+      put(2 * l, pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y));
+      put(2 * l + D / 2, pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y));
+      for (g += HPW; g >= Gq; g -= Gq) ++kv;
     }
   }
 }
@@ -182,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   constexpr int NT = D / 8;                      // 8-wide output tiles
   constexpr int KS = BF ? D / 16 : D / 8;        // k steps of the scores
   extern __shared__ __align__(128) unsigned char sm_raw[];
-  int64_t* pre = reinterpret_cast<int64_t*>(sm_raw + kWarps * kRing);  // [n_req + 1] first tile
+  int32_t* pre = reinterpret_cast<int32_t*>(sm_raw + kWarps * (kRing + kAngles));  // [n_req + 1]
   __shared__ int64_t warp_tot[kWarps];
   __shared__ int cta_err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -216,12 +208,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       if (w < warp) base += warp_tot[w];
       carry += warp_tot[w];
     }
-    if (r < p.n_req) pre[r] = base + inc - v;
+    if (r < p.n_req) pre[r] = (int32_t)(base + inc - v);
     __syncthreads();
   }
-  if (tid == 0) pre[p.n_req] = carry;
+  if (tid == 0) pre[p.n_req] = (int32_t)carry;
   __syncthreads();
-  const int64_t total = carry;
+  // (2^31 tiles are hours of work: a list that long is refused rather than counted in 64 bits)
+  if (carry > INT_MAX) err = kErrCtxOverflow;
+  const int64_t total = carry > INT_MAX ? 0 : carry;
   const int S = (int)max((int64_t)1, min((int64_t)S_max, total / kMinTiles));
   const int w_all = blockIdx.x * kWarps + warp;
   const int s = w_all / p.h_kv, head = w_all % p.h_kv;
@@ -236,7 +230,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     // where a tile of the list lies
     struct Cur {
       int r, blk, t, TPP, CT, nb;
+      int last;  // last local row that the block's last token sees
       PagedReq q;
+    };
+    auto set_last = [&](Cur& c) {
+      c.last = min(c.q.L - c.q.T + min((c.blk * kRows + kRows - 1) / Gq, c.q.T - 1), c.q.L - 1);
     };
     auto enter = [&](Cur& c, int r) {  // request r's geometry (r has tiles)
       int ignore = 0;
@@ -249,16 +247,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     auto step = [&](Cur& c) {  // the next tile of the list (only called when there is one)
       if (++c.t < c.TPP) return;
       c.t = 0;
-      if (++c.blk < c.nb) return;
-      c.blk = 0;
-      int r = c.r + 1;
-      while (pre[r + 1] == pre[r]) ++r;
-      enter(c, r);
-    };
-    // last local row that the block's last token sees
-    auto block_last = [&](const Cur& c) {
-      const int t_last = min((c.blk * kRows + kRows - 1) / Gq, c.q.T - 1);
-      return c.q.L - c.q.T + t_last;
+      if (++c.blk == c.nb) {
+        c.blk = 0;
+        int r = c.r + 1;
+        while (pre[r + 1] == pre[r]) ++r;
+        enter(c, r);
+      }
+      set_last(c);
     };
     Cur ld;
     {
@@ -269,9 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         else hi = mid;
       }
       enter(ld, lo);
-      const int64_t off = x0 - pre[lo];
-      ld.blk = (int)(off / ld.TPP);
-      ld.t = (int)(off % ld.TPP);
+      const int off = (int)x0 - pre[lo];
+      ld.blk = off / ld.TPP;
+      ld.t = off % ld.TPP;
+      set_last(ld);
     }
     Cur cu = ld;  // the tile being computed; ld is the tile being loaded
 
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     auto lookup = [&](const Cur& c) -> int {
       if (c.t < c.CT) return 0;
       const int k0 = (c.t - c.CT) * KT;
-      if (k0 >= c.q.L || k0 > block_last(c)) return -1;  // nothing of it is seen
+      if (k0 > c.last) return -1;  // nothing of it is seen
       return __ldg(p.table + (int64_t)c.r * p.max_pages + (k0 >> p.page_shift));
     };
     int page = lookup(ld);
@@ -296,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         valid = min(KT, c.q.C - c.t * KT);
       } else {
         const int k0 = (c.t - c.CT) * KT;
-        if (k0 < c.q.L && k0 <= block_last(c)) {
+        if (k0 <= c.last) {
           if (page < 0 || page >= n_slot_pages) {
             err = kErrBadIndex;
           } else {
@@ -346,52 +342,99 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       const int t_end = (int)min((int64_t)cu.TPP, (int64_t)cu.t + (n_tiles - v));
       const bool ends = t_end == cu.TPP;
       const int nrow = min(kRows, (int)min((long long)kRows, (long long)cu.q.T * Gq - (long long)cu.blk * kRows));
-      int vis[2];  // last local row that query rows gr and gr + 8 see
+      // The block's queries, rotated. A lane's fragment elements of dims i and i + D/2 are its
+      // own, and the angles of a token are the same for all its heads: the warp computes them
+      // once into a table in shared memory, some tokens at a time (the first exactly, the next
+      // ones by rotating on: at most 15 steps of 2^-23).
+      int vis[2], row_tok[2];  // last local row that query rows gr and gr + 8 see; their tokens
+      const int tok0 = cu.blk * kRows / Gq;
+      const int n_tok = (cu.blk * kRows + nrow - 1) / Gq - tok0 + 1;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int row = cu.blk * kRows + min(gr + 8 * hf, nrow - 1);
-        const int tok = row / Gq, hq = head * Gq + row % Gq;
-        const int j = cu.q.L - cu.q.T + tok;
-        vis[hf] = j;
-        const T* src = static_cast<const T*>(p.Q) + (int64_t)(cu.q.a + tok) * p.q_stride + hq * D;
-        const int64_t pos = (int64_t)p.pos0 + j;
-        // a lane's fragment elements of dims i and i + D/2 are its own: it rotates them itself
-        if constexpr (BF) {
+        const int tok = row / Gq;
+        vis[hf] = cu.q.L - cu.q.T + tok;
+        row_tok[hf] = tok - tok0;
+        const T* src = static_cast<const T*>(p.Q) + (int64_t)(cu.q.a + tok) * p.q_stride +
+                       (head * Gq + row % Gq) * D;
+        if constexpr (BF) {  // the values as stored; turned below
 #pragma unroll
-          for (int kk = 0; kk < KS / 2; ++kk) {
+          for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = kk * 16 + e * 8 + 2 * t4;
-              const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(src + i));
-              const uint32_t hi = __ldg(reinterpret_cast<const uint32_t*>(src + i + D / 2));
-              float2 c0 = make_float2(1.f, 0.f), c1 = c0;
-              if (p.rope) {
-                c0 = rot_turns(pos, p.rope_turns[i]);
-                c1 = rot_turns(pos, p.rope_turns[i + 1]);
-              }
-              const float a0 = __uint_as_float(lo << 16), a1 = __uint_as_float(lo & 0xFFFF0000u);
-              const float b0 = __uint_as_float(hi << 16), b1 = __uint_as_float(hi & 0xFFFF0000u);
-              // rounded to bf16 for the tensor cores, as the keys were when appended
-              qh[kk][hf + 2 * e] = pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
-              qh[kk + KS / 2][hf + 2 * e] =
-                  pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
-            }
-          }
+            for (int e = 0; e < 2; ++e)
+              qh[kk][hf + 2 * e] =
+                  __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + e * 8 + 2 * t4));
         } else {
 #pragma unroll
-          for (int kk = 0; kk < KS / 2; ++kk) {
+          for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = kk * 8 + e * 4 + t4;
-              const float a0 = __ldg(reinterpret_cast<const float*>(src) + i);
-              const float b0 = __ldg(reinterpret_cast<const float*>(src) + i + D / 2);
-              const float2 c0 = p.rope ? rot_turns(pos, p.rope_turns[i]) : make_float2(1.f, 0.f);
-              split_tf32(a0 * c0.x - b0 * c0.y, qh[kk][hf + 2 * e], ql[kk][hf + 2 * e]);
-              split_tf32(b0 * c0.x + a0 * c0.y, qh[kk + KS / 2][hf + 2 * e],
-                         ql[kk + KS / 2][hf + 2 * e]);
+            for (int e = 0; e < 2; ++e)
+              qh[kk][hf + 2 * e] =
+                  __ldg(reinterpret_cast<const uint32_t*>(src + kk * 8 + e * 4 + t4));
+        }
+      }
+      if (p.rope) {
+        constexpr int PL = D / 64;                  // RoPE pairs of a lane: l, l + 32
+        constexpr int CAP = kAngles / (D / 2 * 8);  // tokens the table holds
+        float2* table = reinterpret_cast<float2*>(sm_raw + kWarps * kRing + warp * kAngles);
+        float2 cs[PL], st[PL];
+#pragma unroll 1
+        for (int t0 = 0; t0 < n_tok; t0 += CAP) {
+          const int64_t pos = (int64_t)p.pos0 + cu.q.L - cu.q.T + tok0 + t0;
+#pragma unroll
+          for (int e = 0; e < PL; ++e) {
+            cs[e] = rot_turns(pos, p.rope_turns[lane + 32 * e]);
+            if (n_tok > 1) st[e] = rot_turns(1, p.rope_turns[lane + 32 * e]);
+          }
+#pragma unroll 1
+          for (int t = 0; t < min(CAP, n_tok - t0); ++t) {
+#pragma unroll
+            for (int e = 0; e < PL; ++e) {
+              table[t * (D / 2) + lane + 32 * e] = cs[e];
+              if (n_tok > 1)
+                cs[e] = make_float2(cs[e].x * st[e].x - cs[e].y * st[e].y,
+                                    cs[e].y * st[e].x + cs[e].x * st[e].y);
             }
           }
+          __syncwarp();
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int t = row_tok[hf] - t0;
+            if (t < 0 || t >= CAP) continue;
+            const float2* ang = table + t * (D / 2);
+#pragma unroll
+            for (int kk = 0; kk < KS / 2; ++kk) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint32_t& lo = qh[kk][hf + 2 * e];
+                uint32_t& hi = qh[kk + KS / 2][hf + 2 * e];
+                if constexpr (BF) {
+                  // rounded to bf16 for the tensor cores, as the keys were when appended
+                  const float4 c = *reinterpret_cast<const float4*>(ang + kk * 16 + e * 8 + 2 * t4);
+                  const float a0 = __uint_as_float(lo << 16), a1 = __uint_as_float(lo & 0xFFFF0000u);
+                  const float b0 = __uint_as_float(hi << 16), b1 = __uint_as_float(hi & 0xFFFF0000u);
+                  lo = pack_bf16(a0 * c.x - b0 * c.y, a1 * c.z - b1 * c.w);
+                  hi = pack_bf16(b0 * c.x + a0 * c.y, b1 * c.z + a1 * c.w);
+                } else {
+                  const float2 c = ang[kk * 8 + e * 4 + t4];
+                  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
+                  lo = __float_as_uint(a * c.x - b * c.y);
+                  hi = __float_as_uint(b * c.x + a * c.y);
+                }
+              }
+            }
+          }
+          __syncwarp();  // the table is filled anew
         }
+      }
+      if constexpr (!BF) {
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __uint_as_float(qh[kk][e]);
+            split_tf32(x, qh[kk][e], ql[kk][e]);
+          }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -400,7 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       m[0] = m[1] = -INFINITY;
       l[0] = l[1] = 0.f;
       const int first_vis = cu.q.L - cu.q.T + cu.blk * kRows / Gq;  // of the block's first token
-      const int last_vis = block_last(cu);
 
       for (; cu.t < t_end; ++cu.t, ++v) {
         cp_wait<NST - 2>();
@@ -409,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         cp_commit();
         const bool ctx = cu.t < cu.CT;
         const int k0 = ctx ? cu.t * KT : (cu.t - cu.CT) * KT;
-        if (!ctx && (k0 >= cu.q.L || k0 > last_vis)) continue;  // nothing visible
+        if (!ctx && k0 > cu.last) continue;  // nothing visible
         const bool full = ctx ? k0 + KT <= cu.q.C : k0 + KT - 1 <= first_vis;
         const uint32_t kb = ring + (uint32_t)(v % NST) * (2 * TILE), vb = kb + TILE;
         constexpr int NK = KT / 8;
@@ -570,42 +612,51 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
 // over its segments i in a fixed order. The first S * h_kv CTAs take the warp-level kernel's
 // blocks of 16 rows (a row's segments shared among the warps), kTcParts CTAs a range the tcgen05
 // kernel's blocks of up to 256 rows (a warp a row). Few bytes: latency-bound.
-template <int EL> struct Fold {
+template <int EL> struct Fold {   // a lane holds EL consecutive elements of the row
+  static constexpr int U = 4;
   float M = -INFINITY, L = 0.f, acc[EL];
   __device__ __forceinline__ Fold() {
 #pragma unroll
     for (int e = 0; e < EL; ++e) acc[e] = 0.f;
   }
-  // segments i, i + step, i + 2 step, .. < n, four loads in flight; slot(i): the row's partial
+  static __device__ __forceinline__ void load(float (&v)[EL], const float* at) {
+    if constexpr (EL == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(at);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(at);
+      v[0] = x.x; v[1] = x.y;
+    }
+  }
+  // segments i, i + step, i + 2 step, .. < n, U loads in flight; slot(i): the row's partial
   template <typename F>
   __device__ __forceinline__ void run(int i, int step, int n, const float* ml, const float* o,
                                       int lane, F slot) {
-    for (; i < n; i += step * 4) {
-      float mi[4], li[4], ov[4][EL];
+#pragma unroll 1
+    for (; i < n; i += step * U) {
+      float2 ml2[U];
+      float ov[U][EL];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int j = i + u * step;
-        mi[u] = -INFINITY;
-        li[u] = 0.f;
+        ml2[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int e = 0; e < EL; ++e) ov[u][e] = 0.f;
         if (j < n) {
           const int64_t at = slot(j);
-          mi[u] = ml[at * 2];
-          li[u] = ml[at * 2 + 1];
-#pragma unroll
-          for (int e = 0; e < EL; ++e) ov[u][e] = o[at * (EL * 32) + e * 32 + lane];
+          ml2[u] = *reinterpret_cast<const float2*>(ml + at * 2);
+          load(ov[u], o + at * (EL * 32) + lane * EL);
         }
       }
       float Mn = M;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) Mn = fmaxf(Mn, mi[u]);
+      for (int u = 0; u < U; ++u) Mn = fmaxf(Mn, ml2[u].x);
       rescale(Mn);
       const float use = Mn == -INFINITY ? 0.f : Mn;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float w = ex2(mi[u] - use);
-        L = fmaf(li[u], w, L);
+      for (int u = 0; u < U; ++u) {
+        const float w = ex2(ml2[u].x - use);
+        L = fmaf(ml2[u].y, w, L);
 #pragma unroll
         for (int e = 0; e < EL; ++e) acc[e] = fmaf(ov[u][e], w, acc[e]);
       }
@@ -618,16 +669,24 @@ template <int EL> struct Fold {
     for (int e = 0; e < EL; ++e) acc[e] *= a;
     M = Mn;
   }
-  template <typename T> __device__ __forceinline__ void store(T* out, int lane) const {
+  template <typename T> __device__ __forceinline__ void store(T* row, int lane) const {
     const float inv = L > 0.f ? 1.f / L : 0.f;
+    T* out = row + lane * EL;
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int e = 0; e < EL; ++e) out[e * 32 + lane] = Elem<T>::from_f(acc[e] * inv);
+      for (int e = 0; e < EL; e += 2)
+        *reinterpret_cast<uint32_t*>(out + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EL; e += 2)
+        *reinterpret_cast<float2*>(out + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+    }
   }
 };
-constexpr int kTcParts = 32;  // CTAs per range of the tcgen05 kernel: 8 of its 256 rows each
+constexpr int kTcParts = 256 * 32 / kMergeThreads;  // CTAs per range of the tcgen05 kernel: a warp a row
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedAttendParams p, int S,
+__global__ void __launch_bounds__(kMergeThreads, 2) paged_merge_kernel(PagedAttendParams p, int S,
                                                                     int n_cta) {
   constexpr int EL = D / 32;  // elements a lane holds
   constexpr int W = kMergeThreads / 32;
@@ -758,7 +817,7 @@ PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int
   pl.tc_ml_bytes = al((size_t)pl.tc_grid * 2 * 256 * 2 * sizeof(float));
   pl.tc_o_bytes = al((size_t)pl.tc_grid * 2 * 256 * d * sizeof(float));
   pl.q_bytes = tc ? al((size_t)n_rows * h_q * d * 2) : 0;
-  pl.smem = pga::kWarps * pga::kRing + ((size_t)n_req + 1) * sizeof(int64_t);
+  pl.smem = pga::kWarps * (pga::kRing + pga::kAngles) + ((size_t)n_req + 1) * sizeof(int32_t);
   return pl;
 }
 
