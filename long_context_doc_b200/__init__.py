@@ -679,23 +679,20 @@ def _explain_pool(what: str, K_pages, V_pages):
                     V_pages=(V_pages, K_pages.dtype, None))
 
 
-class _on:
-    """Makes device ``index`` current for a launch (nothing to do when it is, or for -1)."""
-    __slots__ = ("index", "back")
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.back = -1
-        if self.index >= 0:
-            self.back = torch.cuda.current_device()
-            if self.back != self.index:
-                torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back >= 0 and self.back != self.index:
-            torch.cuda.set_device(self.back)
+def _launch(dev: int, stream, f, *args):
+    """f(*args, stream) with device ``dev`` current, on ``stream`` or the device's current one."""
+    if stream is None:
+        # the raw handle of torch.cuda.current_stream(dev), at a twentieth of its 3 us
+        stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if dev < 0 or torch.cuda.current_device() == dev:
+        status = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, stream)
+    if status:
+        _check(status)
 
 
 def page_plan_buffers(n_req: int, max_rows: int, device="cuda") -> dict:
@@ -731,9 +728,11 @@ def page_plan(target, length, n_free, block_table, free_list, page_size: int, ma
                                                  zip(names, wanted)})
     if ws.get_device() != dev or not ws.is_contiguous():
         _explain_arrays("page_plan", dev, ws=(ws, None, None))
-    with _on(dev):
-        msa_page_plan(target, length, n_free, page_size, block_table, free_list, out["length"],
-                      out["n_free"], out["row_start"], out["slot_map"], out["row_pos"], ws, stream)
+    _launch(dev, stream, lib.msa_page_plan, target.data_ptr(), length.data_ptr(),
+            n_free.data_ptr(), n_req, page_size, block_table.shape[1], free_list.numel(), max_rows,
+            block_table.data_ptr(), free_list.data_ptr(), out["length"].data_ptr(),
+            out["n_free"].data_ptr(), out["row_start"].data_ptr(), out["slot_map"].data_ptr(),
+            out["row_pos"].data_ptr(), ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -765,9 +764,11 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
                         row_pos=(row_pos, i32, None), ws=(ws, None, None))
         rows = min(slot_map.numel(), row_pos.numel())
         _need("paged_append", rows >= n_rows, f"slot_map and row_pos cover {rows} of {n_rows} rows")
-    with _on(dev):
-        msa_paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, rope_base, ws,
-                         stream)
+    n_pages, page = K_pages.shape[:2]
+    _launch(dev, stream, lib.msa_paged_append, K_pages.data_ptr(), V_pages.data_ptr(), n_pages,
+            page, slot_map.data_ptr(), row_pos.data_ptr(), K_new.data_ptr(), V_new.data_ptr(),
+            K_new.stride(0), V_new.stride(0), n_rows, h_kv, d, dtype_code(K_pages), pos0,
+            rope_base, ws.data_ptr(), ws.nbytes)
     return ws
 
 
@@ -813,21 +814,20 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
                         length=(length, i32, n_req), block_table=(block_table, i32, None),
                         ctxK=(ctxK, dt, None), ctxV=(ctxV, dt, None),
                         ctx_len=(ctx_len, i32, n_req))
-    with _on(dev):
-        if ws is None:
-            ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q),
-                                                max_ctx, max_pages, page), Q.device)
-        elif ws.get_device() != dev or not ws.is_contiguous():
-            _explain_arrays("paged_attend", dev, ws=(ws, None, None))
-        st = _s(stream)
-        status = lib.msa_paged_attend(
-            Q.data_ptr(), Q.stride(0), n_rows, h_q, row_start.data_ptr(), length.data_ptr(), n_req,
-            K_pages.data_ptr(), V_pages.data_ptr(), n_pages, page, block_table.data_ptr(),
-            max_pages, None if ctxK is None else ctxK.data_ptr(),
-            None if ctxK is None else ctxV.data_ptr(),
-            None if ctxK is None else ctx_len.data_ptr(), max_ctx, h_kv, d, dtype_code(Q), pos0,
-            rope_base, scale, O.data_ptr(), ws.data_ptr(), ws.nbytes, st)
-    _check(status)
+    if ws is None:
+        ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q), max_ctx,
+                                            max_pages, page), Q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        _explain_arrays("paged_attend", dev, ws=(ws, None, None))
+    if ctxK is None:
+        mem = (None, None, None)
+    else:
+        mem = (ctxK.data_ptr(), ctxV.data_ptr(), ctx_len.data_ptr())
+    _launch(dev, stream, lib.msa_paged_attend, Q.data_ptr(), Q.stride(0), n_rows, h_q,
+            row_start.data_ptr(), length.data_ptr(), n_req, K_pages.data_ptr(),
+            V_pages.data_ptr(), n_pages, page, block_table.data_ptr(), max_pages, *mem, max_ctx,
+            h_kv, d, dtype_code(Q), pos0, rope_base, scale, O.data_ptr(), ws.data_ptr(),
+            ws.nbytes)
     return O
 
 

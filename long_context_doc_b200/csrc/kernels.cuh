@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <string>
@@ -326,6 +327,19 @@ cudaError_t launch_aux_routing_loss(const void* Q_r, int B, int T, int h_qr, con
                                     cudaStream_t st);
 
 // ---- paged.cu: the paged local context (block tables, slot maps, append)
+// Lets a kernel use up to `bytes` of dynamic shared memory (cudaFuncSetAttribute, made once per
+// device and kernel: about 1 us of the host's time a call otherwise). `done` is a bit per device.
+inline cudaError_t allow_smem_once(const void* kernel, size_t bytes,
+                                   std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 constexpr int kPagedMaxReq = 4096;  // requests of one call (their prefix sums fit shared memory)
 struct PagePlanParams {
   const int32_t* target;   // [n_req] lengths wanted

@@ -283,8 +283,9 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendParams p) 
 cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t st) {
   const int ctas = p.max_rows <= pgd::kPlanOneCta ? 1 : pgd::kPlanCluster;
   const size_t smem = sizeof(int32_t) * (5 * (size_t)p.n_req + 3);
-  cudaError_t e = cudaFuncSetAttribute(pgd::page_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(pgd::page_plan_kernel),
+                                  sizeof(int32_t) * (5 * (size_t)kPagedMaxReq + 3), ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);

@@ -34,6 +34,8 @@ constexpr int kRing = 24576;        // bytes of a warp's ring
 constexpr int kMinTiles = 2;        // a range is at least this many tiles
 constexpr int kAngles = 2048;       // bytes of a warp's angle table: the tokens of a query block
 constexpr int kMergeThreads = 512;
+constexpr size_t kMaxSmem =
+    kWarps * (size_t)(kRing + kAngles) + (kPagedMaxReq + 1) * sizeof(int32_t);
 
 template <typename T, int D> struct Geo {
   static constexpr int KT = sizeof(T) == 2 ? 16 : 8;      // keys of a tile
@@ -115,18 +117,31 @@ __device__ __forceinline__ int range_of(int64_t y, int64_t x, int S) {
 
 // The queries of the requests that the tcgen05 kernel serves, rotated and rounded to bf16, in
 // its operand layout: per KV head and 64 dims the rows (token, query head of the group) one after
-// another, 16-byte chunk c of a row at c ^ (row within its block & 7). A warp takes a token, a
-// lane the RoPE pairs 2l, 2l + 1 of each of its heads (D = 64: of every other head).
+// another, 16-byte chunk c of a row at c ^ (row within its block & 7). A warp takes 16 heads of a
+// token (their loads in flight together): its angles once into the warp's table, then a lane one
+// 16-byte chunk of the lower half of a head and its partner half a head on.
 template <int D>
 __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w, int n_warps,
-                                               int lane) {
-  constexpr int LPH = D / 4;       // lanes of a head
-  constexpr int HPW = 32 / LPH;    // heads a warp takes at once
+                                               int lane, float2* table,
+                                               const unsigned long long* turns) {
+  constexpr int HC = D / 16;       // chunks of half a head
+  constexpr int HPW = 32 / HC;     // heads a warp takes at once
+  constexpr int NI = 16 / HPW;
   const int Gq = p.h_q / p.h_kv, TB = 256 / Gq;
-  const int l = lane % LPH;
+  const int c = lane % HC;
   const int64_t rows = (int64_t)p.n_rows * Gq;
+  const int parts = (p.h_q + 15) / 16;
 #pragma unroll 1
-  for (int i = w; i < p.n_rows; i += n_warps) {
+  for (int64_t unit = w; unit < (int64_t)p.n_rows * parts; unit += n_warps) {
+    const int i = (int)(unit / parts), h0 = (int)(unit % parts) * 16 + lane / HC;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + i * p.q_stride + c * 8;
+    uint4 ra[NI], rb[NI];
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {  // (any row of Q may be read, whoever it belongs to)
+      const int h = min(h0 + k * HPW, p.h_q - 1);
+      ra[k] = __ldg(reinterpret_cast<const uint4*>(src + h * D));
+      rb[k] = __ldg(reinterpret_cast<const uint4*>(src + h * D + D / 2));
+    }
     int lo = 0, hi = p.n_req;      // the request of token i: row_start[lo] <= i < row_start[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -138,31 +153,40 @@ __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w
     const int t = i - q.a;
     if (t < 0 || t >= q.T) continue;
     const int64_t pos = (int64_t)p.pos0 + q.L - q.T + t;
-    float2 c0 = make_float2(1.f, 0.f), c1 = c0;
-    if (p.rope) {
-      c0 = rot_turns(pos, p.rope_turns[2 * l]);
-      c1 = rot_turns(pos, p.rope_turns[2 * l + 1]);
-    }
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        static_cast<const __nv_bfloat16*>(p.Q) + i * p.q_stride);
-    int h = lane / LPH, kv = h / Gq, g = h % Gq;
+#pragma unroll 1
+    for (int e = lane; e < D / 2; e += 32)
+      table[e] = p.rope ? rot_turns(pos, turns[e]) : make_float2(1.f, 0.f);
+    __syncwarp();
+    float4 cs[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cs[e] = *reinterpret_cast<const float4*>(table + c * 8 + 2 * e);
     const int x0 = (t % TB) * Gq;
-#pragma unroll 4
-    for (; h < p.h_q; h += HPW) {
-      const uint32_t lo2 = __ldg(src + h * (D / 2) + l), hi2 = __ldg(src + h * (D / 2) + D / 4 + l);
-      const float a0 = __uint_as_float(lo2 << 16), a1 = __uint_as_float(lo2 & 0xFFFF0000u);
-      const float b0 = __uint_as_float(hi2 << 16), b1 = __uint_as_float(hi2 & 0xFFFF0000u);
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int h = h0 + k * HPW;
+      if (h >= p.h_q) break;
+      using V = Vec<__nv_bfloat16, 8>;
+      float a[8], b[8];
+      V::unpack(ra[k], a);
+      V::unpack(rb[k], b);
+      uint32_t oa[4], ob[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        oa[e] = pack_bf16(a[2 * e] * cs[e].x - b[2 * e] * cs[e].y,
+                          a[2 * e + 1] * cs[e].z - b[2 * e + 1] * cs[e].w);
+        ob[e] = pack_bf16(b[2 * e] * cs[e].x + a[2 * e] * cs[e].y,
+                          b[2 * e + 1] * cs[e].z + a[2 * e + 1] * cs[e].w);
+      }
+      const int kv = h / Gq, g = h % Gq;
       const int x = (x0 + g) & 7;
-      // element e of a head: 64 dims e / 64, chunk (e % 64) / 8
-      auto put = [&](int e, uint32_t v) {
-        unsigned char* row = reinterpret_cast<unsigned char*>(
-            p.q_rot + (((int64_t)kv * (D / 64) + (e >> 6)) * rows + (int64_t)i * Gq + g) * 64);
-        *reinterpret_cast<uint32_t*>(row + ((((e & 63) >> 3) ^ x) << 4) + (e & 7) * 2) = v;
-      };
-      put(2 * l, pack_bf16(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y));
-      put(2 * l + D / 2, pack_bf16(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y));
-      for (g += HPW; g >= Gq; g -= Gq) ++kv;
+      __nv_bfloat16* dst =
+          p.q_rot + ((int64_t)kv * (D / 64) * rows + (int64_t)i * Gq + g) * 64;
+      *reinterpret_cast<uint4*>(dst + ((c ^ x) << 3)) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+      const int cb = c + HC;  // D = 64: the same 64 dims; D = 128: the next ones
+      *reinterpret_cast<uint4*>(dst + (cb >> 3) * rows * 64 + (((cb & 7) ^ x) << 3)) =
+          make_uint4(ob[0], ob[1], ob[2], ob[3]);
     }
+    __syncwarp();  // the table is filled anew
   }
 }
 
@@ -177,8 +201,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   int32_t* pre = reinterpret_cast<int32_t*>(sm_raw + kWarps * (kRing + kAngles));  // [n_req + 1]
   __shared__ int64_t warp_tot[kWarps];
   __shared__ int cta_err;
+  // the angles' fractions, read lane by lane (from the parameters that is a load per lane)
+  __shared__ unsigned long long turns[D / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Gq = p.h_q / p.h_kv;
+  if (tid < D / 2) turns[tid] = p.rope_turns[tid];
 
   // the dependent merge kernel may be set up while this one runs (it waits for the results)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -383,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
           const int64_t pos = (int64_t)p.pos0 + cu.q.L - cu.q.T + tok0 + t0;
 #pragma unroll
           for (int e = 0; e < PL; ++e) {
-            cs[e] = rot_turns(pos, p.rope_turns[lane + 32 * e]);
-            if (n_tok > 1) st[e] = rot_turns(1, p.rope_turns[lane + 32 * e]);
+            cs[e] = rot_turns(pos, turns[lane + 32 * e]);
+            if (n_tok > 1) st[e] = rot_turns(1, turns[lane + 32 * e]);
           }
 #pragma unroll 1
           for (int t = 0; t < min(CAP, n_tok - t0); ++t) {
@@ -601,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   }
   if (head == 0 && lane == 0 && s < S_max) p.tail[s] = tail;
   if constexpr (BF)
-    if (p.tc_rows != INT_MAX) rotate_queries<D>(p, w_all, gridDim.x * kWarps, lane);
+    if (p.tc_rows != INT_MAX) rotate_queries<D>(p, w_all, gridDim.x * kWarps, lane,
+                        reinterpret_cast<float2*>(sm_raw + kWarps * kRing + warp * kAngles), turns);
   if (err) cta_err = err;
   __syncthreads();
   if (tid == 0) p.err_cta[blockIdx.x] = cta_err;
@@ -769,8 +797,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_merge_kernel(PagedAtte
 template <typename T, int D>
 cudaError_t launch(const PagedAttendParams& p, const PagedPlan& pl, cudaStream_t st) {
   auto kfn = paged_attend_kernel<T, D>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(kfn), kMaxSmem, ready);
   if (e != cudaSuccess) return e;
   kfn<<<pl.grid, kThreads, pl.smem, st>>>(p, pl.S);
   e = cudaGetLastError();

@@ -35,6 +35,7 @@ constexpr int kHalf = 128;                // query rows of a half
 constexpr int kThreads = 320;
 constexpr uint32_t kSlice = 128 * 128;    // 128 rows x 64 bf16, 128-byte swizzle: 16 KB
 constexpr uint32_t kBounce = 32 * 128;    // a warp's 128 bytes of 32 rows on their way to memory
+constexpr int kQueue = 4;                 // blocks announced ahead
 constexpr float kRaise = 8.f;
 
 template <int D> struct Cfg {
@@ -178,6 +179,7 @@ struct Work {
   int t0, t1;        // this CTA's tiles of the block, of n_tiles
   int n_tiles;
   int rows;          // query rows of the block
+  int more;          // the share goes on after it
 };
 struct Share {
   int64_t x1, total;  // end of this CTA's share, tiles of the list
@@ -225,6 +227,7 @@ struct Walk {
     w.t0 = from;
     w.t1 = min(w.n_tiles, from + left);
     left -= w.t1 - from;
+    w.more = left > 0;
   }
   __device__ __forceinline__ void enter(Work& w, int r) {
     int ignore = 0;
@@ -298,13 +301,15 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* odone = qfull + 8;      // [2] a block's last P V of the half completed
   uint64_t* pdone = qfull + 10;     // a P V of a one-half block completed
   uint64_t* qempty = qfull + 11;    // [2] a block's last scores of the half formed
-  uint64_t* done = qfull + 13;      // every issued MMA completed
+  uint64_t* bfull = qfull + 13;     // [kQueue] a block of the share announced
+  uint64_t* bempty = bfull + kQueue;  // [kQueue] ... and done with (MMA warp, 8 softmax warps)
+  uint64_t* done = bempty + kQueue;   // every issued MMA completed
   __shared__ int64_t warp_tot[kThreads / 32];
   __shared__ int64_t start_off;
   __shared__ int start_r, cta_err;
   __shared__ int abort_word;
   __shared__ uint32_t tmem_holder;
-  __shared__ Work blocks[8];
+  __shared__ Work blocks[kQueue];
   __shared__ Share share;
   __shared__ int4 tail_item;
   __shared__ int tail_head;
@@ -329,6 +334,10 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       mbar_init(&pfull[i], kHalf);
     }
     mbar_init(pdone, 1);
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&bfull[i], 1);
+      mbar_init(&bempty[i], 9);
+    }
     mbar_init(done, 1);
     abort_word = 0;
     cta_err = 0;
@@ -400,11 +409,13 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_holder;
-    Work w;
-    walk.first(w, start_r, start_off);
+    uint32_t nb = 0;  // blocks of the share taken so far
 
     if (warp == 0) {
-      // ---------------- copies: K then V of each tile, one page (or memory tile) a lane
+      // ---------------- walks the share, announces its blocks and copies: K then V of each tile,
+      // one page (or memory tile) a lane
+      Work w;
+      walk.first(w, start_r, start_off);
       uint32_t seq = 0;
       const int ps = 1 << p.page_shift;
       const int br = min(ps, kN);               // rows of a box
@@ -414,6 +425,17 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       // the rotated queries are written by the grid launched before this one
       asm volatile("griddepcontrol.wait;" ::: "memory");
       while (ok) {
+        if (lane == 0) {
+          const int b = nb % kQueue;
+          ok = nb < kQueue || wait_or_abort(&bempty[b], (nb / kQueue - 1) & 1, &cta_err, abort_flag);
+          if (ok) {
+            blocks[b] = w;
+            mbar_arrive(&bfull[b]);
+          }
+        }
+        ++nb;
+        ok = uniform(ok) != 0;
+        if (!ok) break;
         // the block's queries: a half's rows are consecutive in each slice of its head's
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -477,7 +499,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             }
           }
         }
-        if (walk.left == 0) break;
+        if (!w.more) break;
         walk.next(w, lane);
       }
       // the copies issued land before the CTA can exit
@@ -526,8 +548,13 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       };
       bool ok = true;
       while (true) {
-        const int n = uniform(w.t1 - w.t0);
-        if (uniform(w.rows) > kHalf) {
+        const int bq = nb % kQueue;
+        if (!wait(&bfull[bq], (nb / kQueue) & 1)) break;
+        ++nb;
+        const int n = uniform(blocks[bq].t1 - blocks[bq].t0);
+        const bool two = uniform(blocks[bq].rows) > kHalf, more = uniform(blocks[bq].more) != 0;
+        if (lane == 0) mbar_arrive(&bempty[bq]);
+        if (two) {
           // two halves in alternation, each with its own scores
           ok = wait_ring();
 #pragma unroll
@@ -604,8 +631,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             if (j + 1 == n) commit(&odone[0]);
           }
         }
-        if (!ok || walk.left == 0) break;
-        walk.next(w, lane);
+        if (!ok || !more) break;
       }
       commit(done);
       mbar_wait_bounded(done, 0, &cta_err);
@@ -624,14 +650,15 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       };
       bool ok = true;
       while (true) {
-        // The block's geometry is kept in shared memory for its end and the walk: the tile loop
-        // holds a row of scores in registers.
-        if (lane == 0) blocks[warp - 2] = w;
-        __syncwarp();
+        // the block's geometry stays in shared memory: the tile loop holds a row of scores in
+        // registers
+        ok = wait(&bfull[nb % kQueue], (nb / kQueue) & 1);
+        if (!ok) break;
+        const Work& w = blocks[nb % kQueue];
         const bool two = w.rows > kHalf;
         const bool active = h == 0 || two;
         const int t0 = w.t0, t1 = w.t1, CT = w.CT, n_ctx = w.q.C, n_loc = w.q.L;
-        const bool more = walk.left > 0;
+        const bool more = w.more != 0;
         const bool any_row = h * kHalf + (warp & 3) * 32 < w.rows;  // of the warp
         float m = -INFINITY, l = 0.f;
         if (active) {
@@ -724,15 +751,13 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               const uint32_t q = seq + 2 * (t - t0) + 1;
               ok = wait(&full[q % NS], (q / NS) & 1);
               if (!ok) break;
-              if (lrow >= valid) {
+              unsigned char* v = ring + (q % NS) * C::kTile;
+              const int at = max(valid, 0) * 128;   // every thread of the half 16 bytes a step
+#pragma unroll 1
+              for (int i = at + lrow * 16; i < (int)kSlice; i += kHalf * 16)
 #pragma unroll
-                for (int sl = 0; sl < SL; ++sl) {
-                  uint4* vr = reinterpret_cast<uint4*>(ring + (q % NS) * C::kTile + sl * kSlice +
-                                                       lrow * 128);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) vr[i] = make_uint4(0u, 0u, 0u, 0u);
-                }
-              }
+                for (int sl = 0; sl < SL; ++sl)
+                  *reinterpret_cast<uint4*>(v + sl * kSlice + i) = make_uint4(0u, 0u, 0u, 0u);
               fence_proxy_async_smem();
             }
             fence_before();
@@ -744,8 +769,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         seq += 2 * n;
         if (!two) npd += n;
         if (!ok) break;
-        const Work& b = blocks[warp - 2];
-        const bool begins = t0 == 0, ends = t1 == b.n_tiles;
+        const bool begins = t0 == 0, ends = t1 == w.n_tiles;
         if (active) {
           ok = wait(&odone[h], no++ & 1);
           if (!ok) break;
@@ -758,14 +782,14 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t pslot =
                 ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
-            const int tok = b.blk * walk.TB + row / Gq;
+            const int tok = w.blk * walk.TB + row / Gq;
             unsigned char* dst =
                 whole ? reinterpret_cast<unsigned char*>(
                             static_cast<__nv_bfloat16*>(p.O) +
-                            ((int64_t)(b.q.a + tok) * p.h_q + b.head * Gq + row % Gq) * D)
+                            ((int64_t)(w.q.a + tok) * p.h_q + w.head * Gq + row % Gq) * D)
                       : reinterpret_cast<unsigned char*>(p.tc_o + pslot * D);
             unsigned char* mine = bounce + (warp - 2) * kBounce;
-            const int n_row = b.rows - (row - lane);             // the warp's rows
+            const int n_row = w.rows - (row - lane);             // the warp's rows
             const int steps = whole ? D / 64 : D / 32;
 #pragma unroll 1
             for (int st = 0; st < steps; ++st) {
@@ -807,14 +831,15 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           fence_before();  // O is read before the next block's products
         }
         if (begins && !ends && tid == 64) {  // goes on in the next CTAs' shares
-          const int64_t end = share.x1 - t1 + b.n_tiles;
-          tail_item = make_int4(b.q.a, b.q.T, b.blk,
+          const int64_t end = share.x1 - t1 + w.n_tiles;
+          tail_item = make_int4(w.q.a, w.q.T, w.blk,
                                 (int)((end * share.G + share.total - 1) / share.total - 1));
-          tail_head = b.head;
+          tail_head = w.head;
         }
-        __syncwarp();  // the block is read before the next one takes its place
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bempty[nb % kQueue]);  // the block has been read
+        ++nb;
         if (!more) break;
-        walk.next(w, lane);
       }
     }
     fence_before();
@@ -860,8 +885,8 @@ cudaError_t launch(const PagedAttendParams& p, int grid, cudaStream_t st) {
     mcv = mv;
   }
   auto kfn = paged_attend_tc_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Cfg<D>::smem);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(kfn), Cfg<D>::smem, ready);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
