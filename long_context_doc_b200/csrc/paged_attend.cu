@@ -33,7 +33,7 @@ constexpr int kRows = kPagedWarpRows;  // query rows of a block (the MMA's M)
 constexpr int kRing = 24576;        // bytes of a warp's ring
 constexpr int kMinTiles = 2;        // a range is at least this many tiles
 constexpr int kAngles = 2048;       // bytes of a warp's angle table: the tokens of a query block
-constexpr int kMergeThreads = 512;
+constexpr int kMergeThreads = 256;
 constexpr size_t kMaxSmem =
     kWarps * (size_t)(kRing + kAngles) + (kPagedMaxReq + 1) * sizeof(int32_t);
 
@@ -637,11 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
 
 // Partials of the query blocks that no single range held whole: the block that range s begins
 // and the ranges s + 1 .. tail.w go on with, out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i
-// over its segments i in a fixed order. The first S * h_kv CTAs take the warp-level kernel's
-// blocks of 16 rows (a row's segments shared among the warps), kTcParts CTAs a range the tcgen05
-// kernel's blocks of up to 256 rows (a warp a row). Few bytes: latency-bound.
+// over its segments i in a fixed order. One wave of CTAs: each lists the blocks to fold (of both
+// attention kernels, in the same order in every CTA), then the rows of blocks of few segments are
+// dealt to single warps and those of many segments to whole CTAs (one request split over the
+// machine has few rows of many segments). Few bytes: latency-bound.
+constexpr int kFewSegments = 16;
+constexpr int kQuad = 4;          // rows of a tcgen05 block that a warp folds together
+constexpr int kMaxTails = 2048;   // ranges of both kernels
 template <int EL> struct Fold {   // a lane holds EL consecutive elements of the row
-  static constexpr int U = 4;
+  static constexpr int U = 8;
   float M = -INFINITY, L = 0.f, acc[EL];
   __device__ __forceinline__ Fold() {
 #pragma unroll
@@ -690,6 +694,16 @@ template <int EL> struct Fold {   // a lane holds EL consecutive elements of the
       }
     }
   }
+  __device__ __forceinline__ void add2(float2 a, const float (&oa)[EL], float2 b,
+                                       const float (&ob)[EL]) {
+    const float Mn = fmaxf(M, fmaxf(a.x, b.x));
+    rescale(Mn);
+    const float use = Mn == -INFINITY ? 0.f : Mn;
+    const float wa = ex2(a.x - use), wb = ex2(b.x - use);
+    L = fmaf(b.y, wb, fmaf(a.y, wa, L));
+#pragma unroll
+    for (int e = 0; e < EL; ++e) acc[e] = fmaf(ob[e], wb, fmaf(oa[e], wa, acc[e]));
+  }
   __device__ __forceinline__ void rescale(float Mn) {
     const float a = ex2(M - (Mn == -INFINITY ? 0.f : Mn));
     L *= a;
@@ -711,86 +725,198 @@ template <int EL> struct Fold {   // a lane holds EL consecutive elements of the
     }
   }
 };
-constexpr int kTcParts = 256 * 32 / kMergeThreads;  // CTAs per range of the tcgen05 kernel: a warp a row
-
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads, 2) paged_merge_kernel(PagedAttendParams p, int S,
-                                                                    int n_cta) {
+__global__ void __launch_bounds__(kMergeThreads, 3) paged_merge_kernel(PagedAttendParams p, int S,
+                                                                       int tc_grid, int n_cta) {
   constexpr int EL = D / 32;  // elements a lane holds
   constexpr int W = kMergeThreads / 32;
   __shared__ float sh_o[W][D];
   __shared__ float sh_m[W], sh_l[W];
+  // blocks of few and of many segments: which range, first row task, how many rows
+  __shared__ int16_t item[2][kMaxTails];
+  __shared__ int32_t start[2][kMaxTails + 1];
+  __shared__ unsigned long long warp_tot[W];
+  __shared__ int code;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int Gq = p.h_q / p.h_kv;
+  const int Gq = p.h_q / p.h_kv, TB = 256 / Gq;
+  if (tid == 0) code = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0) {  // the call's status word
-    __shared__ int code;
-    if (tid == 0) code = 0;
-    __syncthreads();
+  if (blockIdx.x == 0)  // the call's status word
     for (int i = tid; i < n_cta; i += kMergeThreads)
       if (p.err_cta[i]) code = p.err_cta[i];
+  auto tail_of = [&](int i) { return i < S ? p.tail[i] : p.tc_tail[2 * (i - S)]; };
+  int n_item[2] = {0, 0}, n_task[2] = {0, 0};
+#pragma unroll 1
+  for (int i0 = 0; i0 < S + tc_grid; i0 += kMergeThreads) {
+    const int i = i0 + tid;
+    int tasks = 0, many = 0;
+    if (i < S + tc_grid) {
+      const int4 t = tail_of(i);
+      if (t.x >= 0) {
+        many = t.w - (i < S ? i : i - S) + 1 > kFewSegments;
+        tasks = i < S ? min(kRows, t.y * Gq - t.z * kRows) * p.h_kv
+                      : min(TB, t.y - t.z * TB) * Gq;
+        if (i >= S && !many) tasks = (tasks + kQuad - 1) / kQuad;
+      }
+    }
+    // one scan of the tasks of both lists (32 bits each), ballots for the items
+    unsigned long long inc = (unsigned long long)tasks << (many ? 32 : 0);
+    const unsigned long long own = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned few_m = __ballot_sync(0xffffffffu, tasks > 0 && !many);
+    const unsigned many_m = __ballot_sync(0xffffffffu, tasks > 0 && many);
+    __shared__ int warp_items[W];
+    if (lane == 31) warp_tot[warp] = inc;
+    if (lane == 0) warp_items[warp] = __popc(few_m) | __popc(many_m) << 16;
     __syncthreads();
-    if (tid == 0) *p.err = code;
-  }
-  const int n_warp_level = S * p.h_kv;
-  if ((int)blockIdx.x >= n_warp_level) {
-    const int s = ((int)blockIdx.x - n_warp_level) / kTcParts;
-    const int row = ((int)blockIdx.x - n_warp_level) % kTcParts * W + warp;
-    const int4 tail = p.tc_tail[2 * s];
-    if (tail.x < 0) return;
-    const int head = p.tc_tail[2 * s + 1].x;
-    const int TB = 256 / Gq;
-    if (row >= min(TB, tail.y - tail.z * TB) * Gq) return;
-    Fold<EL> f;
-    f.run(0, 1, tail.w - s + 1, p.tc_ml, p.tc_o, lane, [&](int i) {
-      return ((int64_t)(s + i) * 2 + (i == 0 ? 1 : 0)) * 256 + row;
-    });
-    const int tok = tail.z * TB + row / Gq, hq = head * Gq + row % Gq;
-    f.store(static_cast<T*>(p.O) + ((int64_t)(tail.x + tok) * p.h_q + hq) * D, lane);
-    return;
-  }
-  const int s = blockIdx.x / p.h_kv, head = blockIdx.x % p.h_kv;
-  const int4 tail = p.tail[s];
-  if (tail.x < 0) return;
-  const int nrow = min(kRows, tail.y * Gq - tail.z * kRows);
-  int wpr = 1;  // warps per row: a power of two, so that a row's warps are neighbours
-  while (wpr * 2 * nrow <= W) wpr *= 2;
-  const int g = warp % wpr;
-  for (int r0 = 0; r0 < nrow; r0 += W / wpr) {
-    const int lr = r0 + warp / wpr;
-    const bool live = lr < nrow;
-    Fold<EL> f;
-    if (live)  // the tail slot of s, then the head slots
-      f.run(g, wpr, tail.w - s + 1, p.part_ml, p.part_o, lane, [&](int i) {
-        return (((int64_t)(s + i) * 2 + (i == 0 ? 1 : 0)) * p.h_kv + head) * kRows + lr;
-      });
-    if (wpr > 1) {
+    unsigned long long before = 0, all = 0;
+    int items_before = 0, items_all = 0;
 #pragma unroll
-      for (int e = 0; e < EL; ++e) sh_o[warp][e * 32 + lane] = f.acc[e];
-      if (lane == 0) {
-        sh_m[warp] = f.M;
-        sh_l[warp] = f.L;
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) {
+        before += warp_tot[w];
+        items_before += warp_items[w];
       }
-      __syncthreads();
-      if (g == 0) {
-        float Mn = f.M;
-        for (int u = 1; u < wpr; ++u) Mn = fmaxf(Mn, sh_m[warp + u]);
-        f.rescale(Mn);
-        const float use = Mn == -INFINITY ? 0.f : Mn;
-        for (int u = 1; u < wpr; ++u) {
-          const float w = ex2(sh_m[warp + u] - use);
-          f.L = fmaf(sh_l[warp + u], w, f.L);
+      all += warp_tot[w];
+      items_all += warp_items[w];
+    }
+    if (tasks > 0) {
+      const unsigned m = (many ? many_m : few_m) & ((1u << lane) - 1u);
+      const int at = n_item[many] + ((items_before >> (many * 16)) & 0xffff) + __popc(m);
+      item[many][at] = (int16_t)i;
+      start[many][at] = n_task[many] + (int)((before + inc - own) >> (many * 32));
+    }
 #pragma unroll
-          for (int e = 0; e < EL; ++e) f.acc[e] = fmaf(sh_o[warp + u][e * 32 + lane], w, f.acc[e]);
+    for (int k = 0; k < 2; ++k) {
+      n_item[k] += (items_all >> (k * 16)) & 0xffff;
+      n_task[k] += (int)(all >> (k * 32));
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) *p.err = code;
+  // row task t of list k: where its partials and its row of O are
+  struct Row {
+    const float* ml;
+    const float* o;
+    int64_t slot0, slot1, step;  // partial of segment 0, of segment 1, between later ones
+    int n_seg, g0;               // g0: first row's query head of the group (tcgen05 blocks)
+    T* out;
+  };
+  auto locate = [&](int k, int t, int* n_row) {
+    int lo = 0, hi = n_item[k];
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[k][mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    const int i = item[k][lo];
+    int x = t - start[k][lo];
+    const int4 tail = tail_of(i);
+    *n_row = 1;
+    Row r;
+    int tok, hq;
+    if (i < S) {
+      const int nrow = min(kRows, tail.y * Gq - tail.z * kRows);
+      const int head = x / nrow, lr = x % nrow, row = tail.z * kRows + lr;
+      r.ml = p.part_ml;
+      r.o = p.part_o;
+      r.step = (int64_t)2 * p.h_kv * kRows;
+      r.slot0 = i * r.step + (int64_t)(p.h_kv + head) * kRows + lr;  // the tail slot of i,
+      r.slot1 = (i + 1) * r.step + (int64_t)head * kRows + lr;       // then the head slots
+      r.n_seg = tail.w - i + 1;
+      tok = row / Gq;
+      hq = head * Gq + row % Gq;
+    } else {
+      const int s = i - S;
+      if (k == 0) {  // rows x .. x + n_row of the block
+        x *= kQuad;
+        *n_row = min(kQuad, min(TB, tail.y - tail.z * TB) * Gq - x);
+        r.g0 = x % Gq;
+      }
+      r.ml = p.tc_ml;
+      r.o = p.tc_o;
+      r.step = 512;
+      r.slot0 = (int64_t)s * 512 + 256 + x;
+      r.slot1 = (int64_t)(s + 1) * 512 + x;
+      r.n_seg = tail.w - s + 1;
+      tok = tail.z * TB + x / Gq;
+      hq = p.tc_tail[2 * s + 1].x * Gq + x % Gq;
+    }
+    r.out = static_cast<T*>(p.O) + ((int64_t)(tail.x + tok) * p.h_q + hq) * D;
+    return r;
+  };
+#pragma unroll 1
+  for (int t = blockIdx.x * W + warp; t < n_task[0]; t += gridDim.x * W) {
+    int n_row;
+    const Row r = locate(0, t, &n_row);
+    auto slot = [&](int i) { return i == 0 ? r.slot0 : r.slot1 + (i - 1) * r.step; };
+    if (r.ml != p.tc_ml) {
+      Fold<EL> f;
+      f.run(0, 1, r.n_seg, r.ml, r.o, lane, slot);
+      f.store(r.out, lane);
+      continue;
+    }
+    Fold<EL> f[kQuad];  // kQuad rows a segment at a time, two segments' loads in flight
+#pragma unroll 1
+    for (int i = 0; i < r.n_seg; i += 2) {
+      float2 ml2[2][kQuad];
+      float ov[2][kQuad][EL];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < kQuad; ++q) {
+          ml2[u][q] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int e = 0; e < EL; ++e) ov[u][q][e] = 0.f;
+          if (i + u < r.n_seg && q < n_row) {
+            const int64_t at = slot(i + u) + q;
+            ml2[u][q] = *reinterpret_cast<const float2*>(r.ml + at * 2);
+            Fold<EL>::load(ov[u][q], r.o + at * D + lane * EL);
+          }
         }
+#pragma unroll
+      for (int q = 0; q < kQuad; ++q) f[q].add2(ml2[0][q], ov[0][q], ml2[1][q], ov[1][q]);
+    }
+    T* out = r.out;
+#pragma unroll
+    for (int q = 0; q < kQuad; ++q) {
+      if (q < n_row) f[q].store(out, lane);
+      // the next row: the group's next query head, or the next token's first one
+      out += (r.g0 + q + 1) % Gq == 0 ? (int64_t)(p.h_q - Gq + 1) * D : D;
+    }
+  }
+#pragma unroll 1
+  for (int t = blockIdx.x; t < n_task[1]; t += gridDim.x) {
+    int n_row;
+    const Row r = locate(1, t, &n_row);
+    Fold<EL> f;
+    f.run(warp, W, r.n_seg, r.ml, r.o, lane,
+          [&](int i) { return i == 0 ? r.slot0 : r.slot1 + (i - 1) * r.step; });
+#pragma unroll
+    for (int e = 0; e < EL; ++e) sh_o[warp][e * 32 + lane] = f.acc[e];
+    if (lane == 0) {
+      sh_m[warp] = f.M;
+      sh_l[warp] = f.L;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      float Mn = f.M;
+      for (int u = 1; u < W; ++u) Mn = fmaxf(Mn, sh_m[u]);
+      f.rescale(Mn);
+      const float use = Mn == -INFINITY ? 0.f : Mn;
+      for (int u = 1; u < W; ++u) {
+        const float w = ex2(sh_m[u] - use);
+        f.L = fmaf(sh_l[u], w, f.L);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) f.acc[e] = fmaf(sh_o[u][e * 32 + lane], w, f.acc[e]);
       }
-      __syncthreads();
+      f.store(r.out, lane);
     }
-    if (live && g == 0) {
-      const int row = tail.z * kRows + lr;
-      const int tok = row / Gq, hq = head * Gq + row % Gq;
-      f.store(static_cast<T*>(p.O) + ((int64_t)(tail.x + tok) * p.h_q + hq) * D, lane);
-    }
+    __syncthreads();  // the shared rows are written anew
   }
 }
 
@@ -809,7 +935,7 @@ cudaError_t launch(const PagedAttendParams& p, const PagedPlan& pl, cudaStream_t
   }
   // the merge kernel is launched while the attention runs and waits for it on the device
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pl.S * p.h_kv + pl.tc_grid * kTcParts);
+  cfg.gridDim = dim3(pl.grid * 3);  // one wave
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -817,7 +943,8 @@ cudaError_t launch(const PagedAttendParams& p, const PagedPlan& pl, cudaStream_t
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, p, pl.S, pl.grid + pl.tc_grid);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, p, pl.S, pl.tc_grid,
+                            pl.grid + pl.tc_grid);
 }
 
 }  // namespace pga
