@@ -154,14 +154,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Bounded wait by polling (a phase is usually a microsecond or less away): gives up after
-// 2^26 polls, a second or more, or when another role has given up.
+// Bounded wait: gives up after the default limit (a second or so), or when another role has given
+// up. The blocking form: warps that spun on the non-blocking test took issue slots from the other
+// half's softmax (4% of a long chunk's time).
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t par, int* err,
                                               volatile int* abort_flag) {
+  if (mbar_try_wait(bar, par)) return true;
+  const long long t0 = clock64();
 #pragma unroll 1
-  for (uint32_t i = 1; !mbar_test_wait(bar, par); ++i) {
-    if ((i & 63u) == 0u && *abort_flag) return false;
-    if (i >> 26) {
+  while (!mbar_try_wait(bar, par)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kDefaultWaitLimit) {
       set_err(err, kErrWaitTimeout);
       *abort_flag = 1;
       return false;
@@ -571,16 +574,16 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           for (int j = 0; j < n; ++j) {
             const bool last = j + 1 == n;
             const int v = rs;
-            ok = wait(&pfull[0], np[0] & 1) && wait_ring();
+            // the tile's V and the next K first: what follows the probabilities is the critical path
+            ok = wait_ring();
+            advance();
+            ok = ok && (last || wait_ring()) && wait(&pfull[0], np[0] & 1);
             ++np[0];
             if (!ok) break;
             product(0, 0, v, j == 0);
-            advance();
             if (last) {
               commit(&odone[0]);
             } else {
-              ok = wait_ring();
-              if (!ok) break;
               scores(0, 0, 0, rs);
               if (j + 2 == n) commit(&qempty[0]);
             }
