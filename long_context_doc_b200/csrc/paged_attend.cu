@@ -33,12 +33,16 @@ constexpr int kRows = kPagedWarpRows;  // query rows of a block (the MMA's M)
 constexpr int kRing = 24576;        // bytes of a warp's ring
 constexpr int kMinTiles = 2;        // a range is at least this many tiles
 constexpr int kAngles = 2048;       // bytes of a warp's angle table: the tokens of a query block
+constexpr int kReqCache = 256;      // requests whose geometry is kept in shared memory
 constexpr int kMergeThreads = 256;
 constexpr size_t kMaxSmem =
     kWarps * (size_t)(kRing + kAngles) + (kPagedMaxReq + 1) * sizeof(int32_t);
 
 template <typename T, int D> struct Geo {
-  static constexpr int KT = sizeof(T) == 2 ? 16 : 8;      // keys of a tile
+  // keys of a tile: 8 KB of K and V (16 keys at bf16, d = 64, paid the softmax's shuffles and the
+  // copies' bookkeeping for 4 KB)
+  static constexpr int KT = sizeof(T) == 2 ? 2048 / D : 8;
+  static constexpr int MIN_TILES = sizeof(T) == 2 ? kMinTiles : 3 * kMinTiles;
   static constexpr int RB = D * (int)sizeof(T);            // bytes of a key row of one head
   static constexpr int TILE = KT * RB;                     // K (or V) of a tile
   static constexpr int NST = kRing / (2 * TILE);           // stages of the ring
@@ -199,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   constexpr int KS = BF ? D / 16 : D / 8;        // k steps of the scores
   extern __shared__ __align__(128) unsigned char sm_raw[];
   int32_t* pre = reinterpret_cast<int32_t*>(sm_raw + kWarps * (kRing + kAngles));  // [n_req + 1]
+  // requests as paged_req has them, where they are few (the space a longer prefix list takes)
+  PagedReq* reqs = reinterpret_cast<PagedReq*>(pre + kReqCache + 4);
   __shared__ int64_t warp_tot[kWarps];
   __shared__ int cta_err;
   // the angles' fractions, read lane by lane (from the parameters that is a load per lane)
@@ -219,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     int64_t v = 0;
     if (r < p.n_req) {
       const PagedReq q = paged_req(p, r, 0, p.tc_rows, &err);
+      if (p.n_req <= kReqCache) reqs[r] = q;
       v = (int64_t)(((long long)q.T * Gq + kRows - 1) / kRows) * block_tiles<KT>(q);
     }
     int64_t inc = v;
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   // (2^31 tiles are hours of work: a list that long is refused rather than counted in 64 bits)
   if (carry > INT_MAX) err = kErrCtxOverflow;
   const int64_t total = carry > INT_MAX ? 0 : carry;
-  const int S = (int)max((int64_t)1, min((int64_t)S_max, total / kMinTiles));
+  const int S = (int)max((int64_t)1, min((int64_t)S_max, total / G::MIN_TILES));
   const int w_all = blockIdx.x * kWarps + warp;
   const int s = w_all / p.h_kv, head = w_all % p.h_kv;
   const int64_t x0 = s < S ? range_start(total, s, S) : total;
@@ -253,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
 
   if (n_tiles > 0) {
     const uint32_t ring = smem_u32(sm_raw) + warp * kRing;
-    const int n_slot_pages = p.n_pages;
     // where a tile of the list lies
     struct Cur {
       int r, blk, t, TPP, CT, nb;
@@ -266,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     auto enter = [&](Cur& c, int r) {  // request r's geometry (r has tiles)
       int ignore = 0;
       c.r = r;
-      c.q = paged_req(p, r, 0, p.tc_rows, &ignore);
+      c.q = p.n_req <= kReqCache ? reqs[r] : paged_req(p, r, 0, p.tc_rows, &ignore);
       c.CT = ctx_tiles<KT>(c.q);
       c.TPP = block_tiles<KT>(c.q);
       c.nb = (int)(((long long)c.q.T * Gq + kRows - 1) / kRows);
@@ -298,36 +304,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     }
     Cur cu = ld;  // the tile being computed; ld is the tile being loaded
 
-    // a tile's page is looked up one tile before its copies go out
-    auto lookup = [&](const Cur& c) -> int {
-      if (c.t < c.CT) return 0;
-      const int k0 = (c.t - c.CT) * KT;
-      if (k0 > c.last) return -1;  // nothing of it is seen
-      return __ldg(p.table + (int64_t)c.r * p.max_pages + (k0 >> p.page_shift));
+    // The block table of the request being loaded, 32 entries at a time: lane i holds that of
+    // page win + i.
+    int win = 0, window = 0;
+    auto look = [&](const Cur& c, bool entered) {  // the window holds the pages of c's tile
+      if (c.t < c.CT) return;
+      const int pg = ((c.t - c.CT) * KT) >> p.page_shift;
+      if (!entered && pg - win >= 0 && pg - win < 31) return;
+      win = pg;
+      window = __ldg(p.table + (int64_t)c.r * p.max_pages + min(pg + lane, p.max_pages - 1));
     };
-    int page = lookup(ld);
+    look(ld, true);
+    int looked = ld.r;  // request the window belongs to (-1: none yet)
+    if (ld.t < ld.CT) looked = -1;
     auto issue = [&](int v) {  // copies of tile v of the range into stage v % NST
       const Cur& c = ld;
       const uint32_t st = ring + (uint32_t)(v % NST) * (2 * TILE);
-      const T* ks = nullptr;
-      const T* vs = nullptr;
+      const int64_t pitch = (int64_t)p.h_kv * RB;
+      // byte offsets of the tile's first row, and of its 17th less 16 rows, in the source
+      int64_t at[2] = {0, 0};
+      const char* ks = nullptr;
+      const char* vs = nullptr;
       int valid = 0;
       if (c.t < c.CT) {
-        const int64_t at = ((int64_t)c.r * p.max_ctx + c.t * KT) * p.h_kv + head;
-        ks = static_cast<const T*>(p.cK) + at * D;
-        vs = static_cast<const T*>(p.cV) + at * D;
+        at[0] = at[1] = (((int64_t)c.r * p.max_ctx + c.t * KT) * p.h_kv + head) * RB;
+        ks = static_cast<const char*>(p.cK);
+        vs = static_cast<const char*>(p.cV);
         valid = min(KT, c.q.C - c.t * KT);
       } else {
         const int k0 = (c.t - c.CT) * KT;
         if (k0 <= c.last) {
-          if (page < 0 || page >= n_slot_pages) {
-            err = kErrBadIndex;
+          look(c, looked != c.r);
+          looked = c.r;
+          valid = min(KT, c.q.L - k0);
+          bool ok = true;
+#pragma unroll
+          for (int e = 0; e < (KT > 16 ? 2 : 1); ++e) {
+            const int k = k0 + 16 * e;  // pages hold 16 rows or more
+            const int page = __shfl_sync(0xffffffffu, window, (k >> p.page_shift) - win);
+            if (16 * e < valid && (page < 0 || page >= p.n_pages)) ok = false;
+            at[e] = ((((int64_t)page << p.page_shift) + (k & ((1 << p.page_shift) - 1)) - 16 * e) *
+                         p.h_kv +
+                     head) * RB;
+          }
+          if (ok) {
+            ks = static_cast<const char*>(p.K_pages);
+            vs = static_cast<const char*>(p.V_pages);
           } else {
-            const int64_t row = ((int64_t)page << p.page_shift) +
-                                (k0 & ((1 << p.page_shift) - 1));
-            ks = static_cast<const T*>(p.K_pages) + (row * p.h_kv + head) * D;
-            vs = static_cast<const T*>(p.V_pages) + (row * p.h_kv + head) * D;
-            valid = min(KT, c.q.L - k0);
+            err = kErrBadIndex;
           }
         }
       }
@@ -335,21 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         constexpr int CPR = RB / 16;      // 16-byte chunks of a row
         constexpr int RPI = 32 / CPR;     // rows a warp instruction copies
         const int c16 = lane % CPR, r0 = lane / CPR;
-        const int64_t pitch = (int64_t)p.h_kv * RB;
 #pragma unroll
         for (int i = 0; i < KT / RPI; ++i) {
           const int row = r0 + i * RPI;
           const bool ok = row < valid;
-          const int64_t off = ok ? row * pitch + c16 * 16 : 0;
+          const int64_t off = ok ? at[i * RPI >= 16 ? 1 : 0] + row * pitch + c16 * 16 : 0;
           const uint32_t dst = st + row * RB + ((c16 ^ (row & 7)) << 4);
-          cp16_zfill(dst, reinterpret_cast<const char*>(ks) + off, ok);
-          cp16_zfill(dst + TILE, reinterpret_cast<const char*>(vs) + off, ok);
+          cp16_zfill(dst, ks + off, ok);
+          cp16_zfill(dst + TILE, vs + off, ok);
         }
       }
-      if (v + 1 < n_tiles) {
-        step(ld);
-        page = lookup(ld);
-      }
+      if (v + 1 < n_tiles) step(ld);
     };
 #pragma unroll
     for (int v = 0; v < NST - 1; ++v) {
@@ -489,10 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
           const int key = ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) {
-            uint32_t b[4];
-            ldsm4(kb + key * RB + (((2 * kk + ((lane >> 3) & 1)) ^ (key & 7)) << 4), b);
-            mma_bf16(sc[0], qh[kk], b[0], b[1]);
-            mma_bf16(sc[1], qh[kk], b[2], b[3]);
+#pragma unroll
+            for (int n = 0; n < NK; n += 2) {
+              uint32_t b[4];
+              ldsm4(kb + (8 * n + key) * RB + (((2 * kk + ((lane >> 3) & 1)) ^ (key & 7)) << 4), b);
+              mma_bf16(sc[n], qh[kk], b[0], b[1]);
+              mma_bf16(sc[n + 1], qh[kk], b[2], b[3]);
+            }
           }
         } else {
           float sl[4] = {0.f, 0.f, 0.f, 0.f};  // the small products apart: two shorter chains
@@ -552,15 +575,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         }
         if constexpr (BF) {
           // the probabilities enter the product in bf16 (their sum above in fp32)
-          const uint32_t a[4] = {pack_bf16(sc[0][0], sc[0][1]), pack_bf16(sc[0][2], sc[0][3]),
-                                 pack_bf16(sc[1][0], sc[1][1]), pack_bf16(sc[1][2], sc[1][3])};
           const int key = lane & 15;
 #pragma unroll
-          for (int nn = 0; nn < NT / 2; ++nn) {
-            uint32_t b[4];
-            ldsm4t(vb + key * RB + (((2 * nn + (lane >> 4)) ^ (key & 7)) << 4), b);
-            mma_bf16(o[2 * nn], a, b[0], b[1]);
-            mma_bf16(o[2 * nn + 1], a, b[2], b[3]);
+          for (int n = 0; n < NK; n += 2) {
+            const uint32_t a[4] = {
+                pack_bf16(sc[n][0], sc[n][1]), pack_bf16(sc[n][2], sc[n][3]),
+                pack_bf16(sc[n + 1][0], sc[n + 1][1]), pack_bf16(sc[n + 1][2], sc[n + 1][3])};
+#pragma unroll
+            for (int nn = 0; nn < NT / 2; ++nn) {
+              uint32_t b[4];
+              ldsm4t(vb + (8 * n + key) * RB + (((2 * nn + (lane >> 4)) ^ (key & 7)) << 4), b);
+              mma_bf16(o[2 * nn], a, b[0], b[1]);
+              mma_bf16(o[2 * nn + 1], a, b[2], b[3]);
+            }
           }
         } else {
           // key order of the k index: t4 -> key 2 t4, t4 + 4 -> key 2 t4 + 1, so that the
@@ -972,7 +999,10 @@ PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int
   pl.tc_ml_bytes = al((size_t)pl.tc_grid * 2 * 256 * 2 * sizeof(float));
   pl.tc_o_bytes = al((size_t)pl.tc_grid * 2 * 256 * d * sizeof(float));
   pl.q_bytes = tc ? al((size_t)n_rows * h_q * d * 2) : 0;
-  pl.smem = pga::kWarps * (pga::kRing + pga::kAngles) + ((size_t)n_req + 1) * sizeof(int32_t);
+  pl.smem = pga::kWarps * (pga::kRing + pga::kAngles) +
+            (n_req <= pga::kReqCache
+                 ? (pga::kReqCache + 4) * sizeof(int32_t) + pga::kReqCache * sizeof(int4)
+                 : ((size_t)n_req + 1) * sizeof(int32_t));
   return pl;
 }
 

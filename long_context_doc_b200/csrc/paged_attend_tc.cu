@@ -306,7 +306,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* qempty = qfull + 11;    // [2] a block's last scores of the half formed
   uint64_t* bfull = qfull + 13;     // [kQueue] a block of the share announced
   uint64_t* bempty = bfull + kQueue;  // [kQueue] ... and done with (MMA warp, 8 softmax warps)
-  uint64_t* done = bempty + kQueue;   // every issued MMA completed
+  uint64_t* phalf = bempty + kQueue;  // [3] the first half of the tile's probabilities written
+  uint64_t* done = phalf + 3;         // every issued MMA completed
   __shared__ int64_t warp_tot[kThreads / 32];
   __shared__ int64_t start_off;
   __shared__ int start_r, cta_err;
@@ -335,6 +336,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
     for (int i = 0; i < 3; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], kHalf);
+      mbar_init(&phalf[i], kHalf);
     }
     mbar_init(pdone, 1);
     for (int i = 0; i < kQueue; ++i) {
@@ -541,13 +543,19 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         }
         commit(&sfull[bar]);
       };
-      auto product = [&](int h, int slot, int st, bool first) {  // O_h (+)= P[slot] V
-        fence_after();
+      // O_h (+)= P[slot] V as the two halves of the tile's probabilities are written
+      auto product = [&](int h, int slot, int bar, uint32_t par, int st, bool first) {
         const uint64_t b = v_desc + st * kStep;
 #pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk)  // 16 keys a step
-          mma_ts(tmem + 256 + h * 128, tmem + slot * 128 + kk * 8, b + kk * (2048 >> 4), idesc_o,
-                 (first && kk == 0) ? 0u : 1u);
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!wait(hf ? &pfull[bar] : &phalf[bar], par)) return false;
+          fence_after();
+#pragma unroll
+          for (int kk = hf * 4; kk < hf * 4 + 4; ++kk)  // 16 keys a step
+            mma_ts(tmem + 256 + h * 128, tmem + slot * 128 + kk * 8, b + kk * (2048 >> 4), idesc_o,
+                   (first && kk == 0) ? 0u : 1u);
+        }
+        return true;
       };
       bool ok = true;
       while (true) {
@@ -577,20 +585,18 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             // the tile's V and the next K first: what follows the probabilities is the critical path
             ok = wait_ring();
             advance();
-            ok = ok && (last || wait_ring()) && wait(&pfull[0], np[0] & 1);
+            ok = ok && (last || wait_ring()) && product(0, 0, 0, np[0] & 1, v, j == 0);
             ++np[0];
             if (!ok) break;
-            product(0, 0, v, j == 0);
             if (last) {
               commit(&odone[0]);
             } else {
               scores(0, 0, 0, rs);
               if (j + 2 == n) commit(&qempty[0]);
             }
-            ok = wait(&pfull[1], np[1] & 1);
+            ok = product(1, 1, 1, np[1] & 1, v, j == 0);
             ++np[1];
             if (!ok) break;
-            product(1, 1, v, j == 0);
             commit(&empty[v]);
             if (last) {
               commit(&odone[1]);
@@ -624,11 +630,11 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
               commit(&empty[rs]);
               advance();
             }
-            ok = wait(&pfull[2 * slot], (slot ? np[2] : np[0]) & 1) && wait(&full[v], vp);
+            ok = wait(&full[v], vp) &&
+                 product(0, slot, 2 * slot, (slot ? np[2] : np[0]) & 1, v, j == 0);
             if (slot) ++np[2];
             else ++np[0];
             if (!ok) break;
-            product(0, slot, v, j == 0);
             commit(&empty[v]);
             commit(pdone);
             if (j + 1 == n) commit(&odone[0]);
@@ -680,6 +686,20 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             ok = wait(&sfull[bar], (alt ? n_alt++ : n_own++) & 1);
             if (!ok) break;
             fence_after();
+            // V rows past the end hold anything: cleared, for 0 * NaN would reach O
+            if (h == 0 && valid < kN) {
+              const uint32_t q = seq + 2 * (t - t0) + 1;
+              ok = wait(&full[q % NS], (q / NS) & 1);
+              if (!ok) break;
+              unsigned char* v = ring + (q % NS) * C::kTile;
+              const int at = max(valid, 0) * 128;   // every thread of the half 16 bytes a step
+#pragma unroll 1
+              for (int i = at + lrow * 16; i < (int)kSlice; i += kHalf * 16)
+#pragma unroll
+                for (int sl = 0; sl < SL; ++sl)
+                  *reinterpret_cast<uint4*>(v + sl * kSlice + i) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
             if (any_row) {
               float sr[128];
 #pragma unroll
@@ -746,22 +766,15 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                   pk[i] = pack_bf16(x.x, x.y);
                 }
                 st8(s_col + ch * 8, pk);
+                if (ch == 3) {
+                  wait_st();
+                  fence_before();
+                  mbar_arrive(&phalf[bar]);
+                }
               }
               wait_st();
-            }
-            // V rows past the end hold anything: cleared, for 0 * NaN would reach O
-            if (h == 0 && valid < kN) {
-              const uint32_t q = seq + 2 * (t - t0) + 1;
-              ok = wait(&full[q % NS], (q / NS) & 1);
-              if (!ok) break;
-              unsigned char* v = ring + (q % NS) * C::kTile;
-              const int at = max(valid, 0) * 128;   // every thread of the half 16 bytes a step
-#pragma unroll 1
-              for (int i = at + lrow * 16; i < (int)kSlice; i += kHalf * 16)
-#pragma unroll
-                for (int sl = 0; sl < SL; ++sl)
-                  *reinterpret_cast<uint4*>(v + sl * kSlice + i) = make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
+            } else {
+              mbar_arrive(&phalf[bar]);
             }
             fence_before();
             mbar_arrive(&pfull[bar]);
