@@ -93,9 +93,8 @@ void rope_fractions(double base, int d, unsigned long long* out) {
 extern "C" {
 
 size_t msa_page_plan_workspace(int32_t n_req, int32_t max_rows) {
-  (void)n_req;
-  (void)max_rows;
-  return kHeader;
+  if (n_req < 0 || max_rows < 0) return kHeader;
+  return kHeader + ((msa::page_plan_sums_bytes(n_req, max_rows) + 255) & ~(size_t)255);
 }
 
 msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
@@ -107,8 +106,9 @@ msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
   msa_status s = check_pool(page_size, n_pages, max_pages, n_req);
   if (s != MSA_OK) return s;
   REQUIRE(max_rows >= 0, MSA_ERR_INVALID_ARG, "max_rows %d", max_rows);
-  REQUIRE(ws != nullptr && ws_bytes >= kHeader && aligned(ws, 256), MSA_ERR_WORKSPACE,
-          "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, kHeader);
+  const size_t need = msa_page_plan_workspace(n_req, max_rows);
+  REQUIRE(ws != nullptr && ws_bytes >= need && aligned(ws, 256), MSA_ERR_WORKSPACE,
+          "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, need);
   REQUIRE(n_free_in && n_free_out && row_start && free_list, MSA_ERR_INVALID_ARG, "null pointer");
   REQUIRE(n_req == 0 || (target_len && len_in && block_table && len_out), MSA_ERR_INVALID_ARG,
           "null pointer");
@@ -131,7 +131,9 @@ msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
   p.max_rows = max_rows;
   p.vec = aligned(slot_map, 16) && aligned(row_pos, 16);
   p.err = static_cast<int*>(ws);
-  return done(msa::launch_page_plan(p, (cudaStream_t)stream), "msa_page_plan launch");
+  if (msa::page_plan_sums_bytes(n_req, max_rows) > 0)
+    p.sums = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + kHeader);
+  return done(msa::launch_page_plan(p, sm_count(), (cudaStream_t)stream), "msa_page_plan launch");
 }
 
 msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,

@@ -354,9 +354,11 @@ struct PagePlanParams {
   int32_t* row_pos;        // [max_rows]
   int n_req, max_pages, n_pages, page_shift, max_rows;
   int vec;                 // slot_map and row_pos 16-byte aligned
+  int32_t* sums;           // workspace for the second launch (null: one launch)
   int* err;
 };
-cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t st);
+size_t page_plan_sums_bytes(int n_req, int max_rows);
+cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st);
 struct PagedAppendParams {
   const void* K_new;       // [n_rows] rows of h_kv * d elements, `stride` elements apart
   const void* V_new;

@@ -6,8 +6,6 @@
 // here the local contexts of many requests of different lengths share one pool of pages of
 // 2^page_shift rows. Request r holds ceil(len_r / page) pages, listed in its row of the block
 // table; pages nobody holds lie on a stack (free_list, its first n_free entries).
-#include <cooperative_groups.h>
-
 #include <algorithm>
 
 #include "common.cuh"
@@ -16,25 +14,35 @@
 namespace msa {
 namespace pgd {
 
-namespace cg = cooperative_groups;
-
 // ------------------------------------------------------------------------------ plan
-// One cluster of one or eight CTAs. With old = len_in, tgt = target, held(x) = ceil(x / page):
-// request r gives back the pages of its table columns [held(tgt), held(old)) or needs pages for
-// the columns [held(old), held(tgt)). Three exclusive sums over the requests (new rows, needed
-// pages, returned pages) fix everything else: the stack after the returns is
-// free_list[0 .. F) followed by the returned pages in request order, and the i-th needed page
-// is the i-th from its top, so with R returns it is returned page R-1-i, or
-// free_list[F-1-(i-R)] for i >= R. Returned pages beyond the needed ones (R > P) stay on the
-// stack at F .. F+R-P. No step depends on another's writes: entries read (below F; columns
-// below held(old)) are never entries written, so one pass over the rows fills the slots and
-// the table together.
-// Every CTA computes the sums for itself (a few microseconds less than a second launch or a
-// trip through memory); the cluster barrier after them is what lets len_out be len_in and
-// nfree_out be nfree_in. Latency-bound throughout.
+// With old = len_in, tgt = target, held(x) = ceil(x / page): request r gives back the pages of its
+// table columns [held(tgt), held(old)) or needs pages for the columns [held(old), held(tgt)).
+// Three exclusive sums over the requests (new rows, needed pages, returned pages) fix everything
+// else: the stack after the returns is free_list[0 .. F) followed by the returned pages in request
+// order, and the i-th needed page is the i-th from its top, so with R returns it is returned page
+// R-1-i, or free_list[F-1-(i-R)] for i >= R. Returned pages beyond the needed ones (R > P) stay on
+// the stack at F .. F+R-P. No step depends on another's writes: entries read (below F; columns
+// below held(old)) are never entries written, so one pass over the rows fills the slots and the
+// table together. One CTA forms the sums and, for up to kPlanOneCta rows, fills the maps itself
+// (one launch; a token for each of 256 requests: 6.5 us); more rows are filled by a second
+// launch that is set up meanwhile (a cluster that did both was held up by its sixteen SMs'
+// arithmetic: 14.6 us for 225,000 rows). Latency-bound.
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCluster = 8;
 constexpr int kPlanOneCta = 4096;  // rows up to which a single CTA fills the maps
+constexpr int kFillThreads = 256;
+
+// what the sums leave for the fill
+struct PlanHead {
+  int rows, F, P, R;
+};
+// the sums of every request, in shared memory or (for the second launch) in the workspace
+struct PlanArrays {
+  const int32_t* row;   // [n + 1] first new row of request r
+  const int32_t* need;  // [n + 1] first needed page
+  const int32_t* back;  // [n + 1] first returned page
+  const int32_t* old;   // [n]
+  const int32_t* tgt;   // [n]
+};
 
 struct PlanSums {
   long long rows, need, back;
@@ -91,22 +99,82 @@ __device__ __forceinline__ int owner(const int32_t* start, int n, int x) {
   return lo;
 }
 
+// The rows of threads gt of nt, four consecutive ones at a time: one search, then a walk along
+// the requests.
+__device__ __forceinline__ void plan_fill(const PagePlanParams& p, const PlanArrays& a,
+                                          const PlanHead& h, int gt, int nt) {
+  const int n = p.n_req, sh = p.page_shift, pm = (1 << sh) - 1;
+  const int F = h.F, R = h.R;
+  auto returned = [&](int q) {  // the q-th returned page
+    const int r = owner(a.back, n, q);
+    const int ht = (int)(((long long)a.tgt[r] + pm) >> sh);
+    return p.table[(int64_t)r * p.max_pages + ht + (q - a.back[r])];
+  };
+  auto popped = [&](int i) {    // the i-th page off the stack
+    return i < R ? returned(R - 1 - i) : p.free_list[F - 1 - (i - R)];
+  };
+  for (int q = gt; q < R - h.P; q += nt) p.free_list[F + q] = returned(q);
+  bool bad_page = false;
+#pragma unroll 1
+  for (int64_t g = gt; g * 4 < p.max_rows; g += nt) {
+    const int i0 = (int)g * 4;
+    int32_t slot[4], pos[4];
+    int r = i0 < h.rows ? owner(a.row, n, i0) : 0;
+    int col = -1;
+    int page = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e;
+      slot[e] = pos[e] = -1;
+      if (i >= h.rows) continue;
+      while (a.row[r + 1] <= i) {
+        ++r;
+        col = -1;
+      }
+      const int at = a.old[r] + (i - a.row[r]);
+      const int c = at >> sh;
+      if (c != col) {
+        col = c;
+        const int ho = (int)(((long long)a.old[r] + pm) >> sh);
+        page = c < ho ? p.table[(int64_t)r * p.max_pages + c] : popped(a.need[r] + (c - ho));
+      }
+      // the first row of a needed page enters it in the table
+      if ((at & pm) == 0) p.table[(int64_t)r * p.max_pages + c] = page;
+      pos[e] = at;
+      const bool ok = page >= 0 && page < p.n_pages;
+      bad_page |= !ok;
+      slot[e] = ok ? (page << sh) + (at & pm) : -1;
+    }
+    if (p.vec && i0 + 3 < p.max_rows) {
+      *reinterpret_cast<int4*>(p.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(p.row_pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + e < p.max_rows) {
+          p.slot_map[i0 + e] = slot[e];
+          p.row_pos[i0 + e] = pos[e];
+        }
+    }
+  }
+  if (bad_page) set_err(p.err, kErrBadIndex);
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PagePlanParams p) {
   extern __shared__ int32_t sm[];
   const int n = p.n_req;
-  int32_t* row_s = sm;                 // [n + 1] first new row of request r
-  int32_t* need_s = sm + (n + 1);      // [n + 1] first needed page
-  int32_t* back_s = sm + 2 * (n + 1);  // [n + 1] first returned page
-  int32_t* old_s = sm + 3 * (n + 1);   // [n]
-  int32_t* tgt_s = old_s + n;          // [n]
+  int32_t* row_s = sm;                 // as PlanArrays
+  int32_t* need_s = sm + (n + 1);
+  int32_t* back_s = sm + 2 * (n + 1);
+  int32_t* old_s = sm + 3 * (n + 1);
+  int32_t* tgt_s = old_s + n;
   __shared__ PlanSums warp_tot[32], chunk_tot;
   __shared__ int bad_len;
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
-  const int nthreads = (int)cluster.num_blocks() * kPlanThreads;
+  const int tid = threadIdx.x;
   const int sh = p.page_shift;
   const int pm = (1 << sh) - 1;
   const long long cap = (long long)p.max_pages << sh;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (tid == 0) bad_len = 0;
   const int F = *p.nfree_in;
@@ -144,79 +212,37 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PagePlanPara
   int code = 0;
   if (bad_len || F < 0 || F > p.n_pages || F + carry.back > p.n_pages) code = kErrBadIndex;
   else if (carry.need > F + carry.back || carry.rows > p.max_rows) code = kErrCtxOverflow;
-  const int rows = code ? 0 : (int)carry.rows;
-  const int P = code ? 0 : (int)carry.need, R = code ? 0 : (int)carry.back;
+  const PlanHead h{code ? 0 : (int)carry.rows, F, code ? 0 : (int)carry.need,
+                   code ? 0 : (int)carry.back};
   if (tid == 0) {
     row_s[n] = (int32_t)carry.rows;
     need_s[n] = (int32_t)carry.need;
     back_s[n] = (int32_t)carry.back;
-    if (rank == 0) *p.err = code;
+    *p.err = code;
+    p.row_start[n] = h.rows;
+    *p.nfree_out = F + h.R - h.P;  // (the count was read before the first barrier)
   }
-  // every CTA has read the lengths and the count, and the status word is started
   __syncthreads();
-  cluster.sync();
-
-  const int gt = rank * kPlanThreads + tid;
-  for (int r = gt; r < n; r += nthreads) {
+  for (int r = tid; r < n; r += kPlanThreads) {
     p.row_start[r] = code ? 0 : row_s[r];
-    p.len_out[r] = code ? p.len_in[r] : tgt_s[r];  // a refused plan keeps the lengths
+    // a refused plan keeps the lengths; len_out may be len_in: every thread reads its own first
+    p.len_out[r] = code ? p.len_in[r] : tgt_s[r];
   }
-  if (gt == 0) {
-    p.row_start[n] = rows;
-    *p.nfree_out = F + R - P;
+  if (p.sums == nullptr) {
+    plan_fill(p, PlanArrays{row_s, need_s, back_s, old_s, tgt_s}, h, tid, kPlanThreads);
+  } else {
+    if (tid == 0) *reinterpret_cast<PlanHead*>(p.sums) = h;
+    for (int i = tid; i < 5 * n + 3; i += kPlanThreads) p.sums[4 + i] = sm[i];
   }
-  // column `col` of request r among its returned pages, and the i-th page off the stack
-  auto returned = [&](int q) {
-    const int r = owner(back_s, n, q);
-    const int ht = (int)(((long long)tgt_s[r] + pm) >> sh);
-    return p.table[(int64_t)r * p.max_pages + ht + (q - back_s[r])];
-  };
-  auto popped = [&](int i) { return i < R ? returned(R - 1 - i) : p.free_list[F - 1 - (i - R)]; };
-  for (int q = gt; q < R - P; q += nthreads) p.free_list[F + q] = returned(q);
+}
 
-  // four consecutive rows a thread: one search, then a walk along the requests
-  bool bad_page = false;
-  for (int i0 = gt * 4; i0 < p.max_rows; i0 += nthreads * 4) {
-    int32_t slot[4], pos[4];
-    int r = i0 < rows ? owner(row_s, n, i0) : 0;
-    int col = -1;
-    int page = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
-      slot[e] = pos[e] = -1;
-      if (i >= rows) continue;
-      while (row_s[r + 1] <= i) {
-        ++r;
-        col = -1;
-      }
-      const int at = old_s[r] + (i - row_s[r]);
-      const int c = at >> sh;
-      if (c != col) {
-        col = c;
-        const int ho = (int)(((long long)old_s[r] + pm) >> sh);
-        page = c < ho ? p.table[(int64_t)r * p.max_pages + c] : popped(need_s[r] + (c - ho));
-      }
-      // the first row of a needed page enters it in the table
-      if ((at & pm) == 0) p.table[(int64_t)r * p.max_pages + c] = page;
-      pos[e] = at;
-      const bool ok = page >= 0 && page < p.n_pages;
-      bad_page |= !ok;
-      slot[e] = ok ? (page << sh) + (at & pm) : -1;
-    }
-    if (p.vec && i0 + 3 < p.max_rows) {
-      *reinterpret_cast<int4*>(p.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      *reinterpret_cast<int4*>(p.row_pos + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i0 + e < p.max_rows) {
-          p.slot_map[i0 + e] = slot[e];
-          p.row_pos[i0 + e] = pos[e];
-        }
-    }
-  }
-  if (bad_page) set_err(p.err, kErrBadIndex);
+__global__ void __launch_bounds__(kFillThreads) page_fill_kernel(PagePlanParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const PlanHead h = *reinterpret_cast<const PlanHead*>(p.sums);
+  const int32_t* a = p.sums + 4;
+  const int n = p.n_req;
+  plan_fill(p, PlanArrays{a, a + (n + 1), a + 2 * (n + 1), a + 3 * (n + 1), a + 3 * (n + 1) + n},
+            h, blockIdx.x * kFillThreads + threadIdx.x, gridDim.x * kFillThreads);
 }
 
 // ------------------------------------------------------------------------------ append
@@ -280,25 +306,30 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendParams p) 
 
 }  // namespace pgd
 
-cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t st) {
-  const int ctas = p.max_rows <= pgd::kPlanOneCta ? 1 : pgd::kPlanCluster;
+size_t page_plan_sums_bytes(int n_req, int max_rows) {
+  return max_rows <= pgd::kPlanOneCta ? 0 : sizeof(int32_t) * (5 * (size_t)n_req + 3 + 4);
+}
+
+cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st) {
   const size_t smem = sizeof(int32_t) * (5 * (size_t)p.n_req + 3);
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(pgd::page_plan_kernel),
                                   sizeof(int32_t) * (5 * (size_t)kPagedMaxReq + 3), ready);
   if (e != cudaSuccess) return e;
+  pgd::page_plan_kernel<<<1, pgd::kPlanThreads, smem, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.sums == nullptr) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(pgd::kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
+  const int per = 4 * pgd::kFillThreads;
+  cfg.gridDim = dim3((unsigned)std::min(((int64_t)p.max_rows + per - 1) / per, (int64_t)sms * 8));
+  cfg.blockDim = dim3(pgd::kFillThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pgd::page_plan_kernel, p);
+  return cudaLaunchKernelEx(&cfg, pgd::page_fill_kernel, p);
 }
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,

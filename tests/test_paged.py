@@ -207,6 +207,8 @@ def test_plan_refuses_on_the_host(msa):
     assert _plan_call(msa, ws=None) == 3
     assert _plan_call(msa, ws=520) == 3
     assert _plan_call(msa, ws_bytes=255) == 3
+    need = msa.msa_page_plan_workspace(2, 5000)
+    assert need > 256 and _plan_call(msa, rows=5000, ws_bytes=need - 1) == 3
     for name in ("target", "len", "nfree", "table", "free", "len_out", "nfree_out", "start",
                  "slot", "pos"):
         assert _plan_call(msa, null=(name,)) == 1, name
@@ -340,7 +342,8 @@ def _run_plan(msa, gpu, target, lens, table, free, n_free, page, max_rows, alias
         v.fill_(-5)
     if alias:
         out["length"], out["n_free"] = length, nf
-    ws = torch.full((256,), 0x5A, dtype=torch.uint8, device=gpu)
+    ws = torch.full((msa.msa_page_plan_workspace(len(lens), max_rows),), 0x5A, dtype=torch.uint8,
+                    device=gpu)
     msa.page_plan(_i32(target, gpu), length, nf, t, f, page, max_rows, out=out, ws=ws)
     got = {k: v.cpu().tolist() for k, v in out.items()}
     return got, t.cpu().numpy(), f.cpu().numpy(), msa.msa_workspace_status(ws)
