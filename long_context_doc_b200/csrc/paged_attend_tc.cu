@@ -417,14 +417,37 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
     uint32_t nb = 0;  // blocks of the share taken so far
 
     if (warp == 0) {
-      // ---------------- walks the share, announces its blocks and copies: K then V of each tile,
-      // one page (or memory tile) a lane
+      // ---------------- walks the share, announces its blocks and copies their queries and tiles,
+      // one page (or memory tile) and 64 dims a lane
       Work w;
       walk.first(w, start_r, start_off);
       uint32_t seq = 0;
       const int ps = 1 << p.page_shift;
       const int br = min(ps, kN);               // rows of a box
       const int half = lane % SL, piece = lane / SL;
+      struct Piece {  // what a lane copies of a tile
+        bool load, ctx;
+        int row;
+        uint32_t bytes;  // of the whole tile
+      };
+      auto put = [&](const Piece& c, int kv) -> bool {  // the tile's K or V into the next slot
+        const int s = seq % NS;
+        if (seq >= NS) {
+          bool free = true;
+          if (lane == 0)
+            free = wait_or_abort(&empty[s], ((seq / NS) - 1) & 1, &cta_err, abort_flag);
+          if (!uniform(free)) return false;
+        }
+        ++seq;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], c.bytes);
+        __syncwarp();
+        if (c.load) {
+          const CUtensorMap* m = c.ctx ? (kv ? &map_cv : &map_ck) : (kv ? &map_v : &map_k);
+          tma3(ring + s * C::kTile + half * kSlice + piece * br * 128, m, half * 64, w.head, c.row,
+               &full[s]);
+        }
+        return true;
+      };
       bool ok = true;
       uint32_t nq[2] = {0, 0};
       // the rotated queries are written by the grid launched before this one
@@ -461,49 +484,36 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           }
           __syncwarp();
         }
+        // K0 K1 V0 K2 V1 .. : a tile's V is needed a softmax after its K, and in a slot it takes up
+        // from its copy's issue on
+        Piece last{};
         for (int t = w.t0; ok && t < w.t1; ++t) {
-          const bool ctx = t < w.CT;
-          const int k0 = (ctx ? t : t - w.CT) * kN;
-          int row = 0;
-          bool load;
-          int rows_per = kN;
-          if (ctx) {
-            load = piece == 0;
-            row = w.r * p.max_ctx + k0;
+          Piece cur;
+          cur.ctx = t < w.CT;
+          const int k0 = (cur.ctx ? t : t - w.CT) * kN;
+          cur.row = 0;
+          if (cur.ctx) {
+            cur.load = piece == 0;
+            cur.row = w.r * p.max_ctx + k0;
           } else {
-            rows_per = br;
             const int k = k0 + piece * br;
-            load = piece < kN / br && k < w.q.L;
-            if (load) {
+            cur.load = piece < kN / br && k < w.q.L;
+            if (cur.load) {
               const int page = __ldg(p.table + (int64_t)w.r * p.max_pages + (k >> p.page_shift));
               if (page < 0 || page >= p.n_pages) {
                 err = kErrBadIndex;
-                load = false;
+                cur.load = false;
               } else {
-                row = (page << p.page_shift) + (k & (ps - 1));
+                cur.row = (page << p.page_shift) + (k & (ps - 1));
               }
             }
           }
-          const uint32_t bytes =
-              __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)rows_per * 128u;
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++seq) {
-            const int s = seq % NS;
-            if (seq >= NS) {
-              if (lane == 0)
-                ok = wait_or_abort(&empty[s], ((seq / NS) - 1) & 1, &cta_err, abort_flag);
-              ok = uniform(ok) != 0;
-              if (!ok) break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
-            __syncwarp();
-            if (load) {
-              const CUtensorMap* m = ctx ? (kv ? &map_cv : &map_ck) : (kv ? &map_v : &map_k);
-              tma3(ring + s * C::kTile + half * kSlice + piece * br * 128, m, half * 64, w.head,
-                   row, &full[s]);
-            }
-          }
+          cur.bytes = __popc(__ballot_sync(0xffffffffu, cur.load)) *
+                      (uint32_t)(cur.ctx ? kN : br) * 128u;
+          ok = put(cur, 0) && (t == w.t0 || put(last, 1));
+          last = cur;
         }
+        ok = ok && put(last, 1);
         if (!w.more) break;
         walk.next(w, lane);
       }
@@ -520,19 +530,12 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                                    ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kHalf >> 4) << 24);
       constexpr uint32_t kStep = C::kTile >> 4;  // ring tile in descriptor units
       const uint64_t q_desc = desc_k(q_s), k_desc = desc_k(ring), v_desc = desc_mn(ring);
-      int rs = 0;                    // next ring tile's stage and phase
-      uint32_t rp = 0;
+      uint32_t seq = 0;              // ring tile of the block's first K
       uint32_t nq[2] = {0, 0}, np[3] = {0, 0, 0};
       auto wait = [&](uint64_t* bar, uint32_t par) {
         return uniform(wait_or_abort(bar, par, &cta_err, abort_flag)) != 0;
       };
-      auto wait_ring = [&]() { return wait(&full[rs], rp); };
-      auto advance = [&]() {
-        if (++rs == NS) {
-          rs = 0;
-          rp ^= 1;
-        }
-      };
+      auto wait_ring = [&](uint32_t q) { return wait(&full[q % NS], (q / NS) & 1); };
       auto scores = [&](int h, int slot, int bar, int st) {  // S[slot] = Q_h K^T
         fence_after();
         const uint64_t a = q_desc + h * kStep, b = k_desc + st * kStep;
@@ -567,79 +570,74 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         if (lane == 0) mbar_arrive(&bempty[bq]);
         if (two) {
           // two halves in alternation, each with its own scores
-          ok = wait_ring();
+          ok = wait_ring(seq);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = ok && wait(&qfull[h], nq[h] & 1);
             ++nq[h];
-            if (ok) scores(h, h, h, rs);
+            if (ok) scores(h, h, h, seq % NS);
             if (ok && n == 1) commit(&qempty[h]);
           }
           if (!ok) break;
-          commit(&empty[rs]);
-          advance();
+          commit(&empty[seq % NS]);
 #pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const bool last = j + 1 == n;
-            const int v = rs;
-            // the tile's V and the next K first: what follows the probabilities is the critical path
-            ok = wait_ring();
-            advance();
-            ok = ok && (last || wait_ring()) && product(0, 0, 0, np[0] & 1, v, j == 0);
+            const uint32_t k = seq + 2 * j + 1, v = last ? k : k + 1;  // next K, this V
+            // both first: what follows the probabilities is the critical path
+            ok = wait_ring(v) && (last || wait_ring(k)) &&
+                 product(0, 0, 0, np[0] & 1, v % NS, j == 0);
             ++np[0];
             if (!ok) break;
             if (last) {
               commit(&odone[0]);
             } else {
-              scores(0, 0, 0, rs);
+              scores(0, 0, 0, k % NS);
               if (j + 2 == n) commit(&qempty[0]);
             }
-            ok = product(1, 1, 1, np[1] & 1, v, j == 0);
+            ok = product(1, 1, 1, np[1] & 1, v % NS, j == 0);
             ++np[1];
             if (!ok) break;
-            commit(&empty[v]);
+            commit(&empty[v % NS]);
             if (last) {
               commit(&odone[1]);
             } else {
-              scores(1, 1, 1, rs);
+              scores(1, 1, 1, k % NS);
               if (j + 2 == n) commit(&qempty[1]);
-              commit(&empty[rs]);
-              advance();
+              commit(&empty[k % NS]);
             }
           }
         } else {
           // one half: its scores alternate between both buffers, a tile ahead of the products
-          ok = wait_ring() && wait(&qfull[0], nq[0] & 1);
+          ok = wait_ring(seq) && wait(&qfull[0], nq[0] & 1);
           ++nq[0];
           if (!ok) break;
-          scores(0, 0, 0, rs);
+          scores(0, 0, 0, seq % NS);
           if (n == 1) commit(&qempty[0]);
-          commit(&empty[rs]);
-          advance();
+          commit(&empty[seq % NS]);
 #pragma unroll 1
           for (int j = 0; j < n; ++j) {
             const int slot = j & 1;
-            const int v = rs;
-            const uint32_t vp = rp;
-            advance();
-            if (j + 1 < n) {
-              ok = wait_ring();
+            const bool last = j + 1 == n;
+            const uint32_t k = seq + 2 * j + 1, v = last ? k : k + 1;
+            if (!last) {
+              ok = wait_ring(k);
               if (!ok) break;
-              scores(0, slot ^ 1, slot ? 0 : 2, rs);
+              scores(0, slot ^ 1, slot ? 0 : 2, k % NS);
               if (j + 2 == n) commit(&qempty[0]);
-              commit(&empty[rs]);
-              advance();
+              commit(&empty[k % NS]);
             }
-            ok = wait(&full[v], vp) &&
-                 product(0, slot, 2 * slot, (slot ? np[2] : np[0]) & 1, v, j == 0);
+            ok = wait_ring(v) &&
+                 product(0, slot, 2 * slot, (slot ? np[2] : np[0]) & 1, v % NS, j == 0);
             if (slot) ++np[2];
             else ++np[0];
             if (!ok) break;
-            commit(&empty[v]);
+            commit(&empty[v % NS]);
             commit(pdone);
-            if (j + 1 == n) commit(&odone[0]);
+            if (last) commit(&odone[0]);
           }
         }
+        seq += 2 * n;
         if (!ok || !more) break;
       }
       commit(done);
@@ -688,7 +686,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             fence_after();
             // V rows past the end hold anything: cleared, for 0 * NaN would reach O
             if (h == 0 && valid < kN) {
-              const uint32_t q = seq + 2 * (t - t0) + 1;
+              const uint32_t q = seq + 2 * (t - t0) + (t + 1 == t1 ? 1 : 2);
               ok = wait(&full[q % NS], (q / NS) & 1);
               if (!ok) break;
               unsigned char* v = ring + (q % NS) * C::kTile;
