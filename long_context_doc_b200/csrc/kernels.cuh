@@ -376,7 +376,7 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, in
                                 cudaStream_t st);
 
 // ---- paged_attend.cu: attention of ragged requests over [routed memory ; paged local context]
-constexpr int kPagedWarpRows = 16;  // query rows per KV head of a block of the warp-level kernel
+constexpr int kPagedWarpRows = 8;  // query rows per KV head of a bf16 block of the warp-level kernel
 struct PagedAttendParams {
   const void* Q;            // [n_rows] rows of h_q * d elements, q_stride elements apart
   int64_t q_stride;
@@ -398,8 +398,8 @@ struct PagedAttendParams {
   int* err;                 // status word, written by the merge kernel
   int* err_cta;             // what each CTA recorded: [grid], then [tc_grid]
   int4* tail;               // [S] the item a range begins and does not end
-  float* part_ml;           // [S][2][h_kv][16][2] partials of the warp-level kernel
-  float* part_o;            // [S][2][h_kv][16][d]
+  float* part_ml;           // [S][2][h_kv][8 or 16][2] partials of the warp-level kernel
+  float* part_o;            // [S][2][h_kv][8 or 16][d]
   int tc_rows;              // requests with more query rows per KV head take the tcgen05 kernel
   int tc_err_at;            // its first entry of err_cta
   int4* tc_tail;            // [tc_grid][2]

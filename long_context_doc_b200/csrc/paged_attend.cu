@@ -7,9 +7,9 @@
 // attends over the request's memory rows and its local rows <= j (keys stored rotated):
 //   O = softmax(scale q . k) v, 0 where nothing is visible.
 //
-// The kernel of this file streams each key row once per 16 query rows and is the one for few
+// The kernel of this file streams each key row once per 16 query rows (bf16: 8) and is the one for few
 // query rows per KV head (single tokens) and for fp32. A warp works alone: for one KV head it
-// takes a contiguous range of the flattened list (request, block of 16 query rows, tile of
+// takes a contiguous range of the flattened list (request, block of query rows, tile of
 // keys), copies the tiles with cp.async into its own ring in shared memory (no barrier between
 // warps), forms the scores and P V with warp-level MMAs (bf16; fp32 as three tf32 products of
 // the operands' high and low parts) and keeps the running maximum and sum of the softmax in
@@ -29,7 +29,7 @@ namespace pga {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = kPagedWarpRows;  // query rows of a block (the MMA's M)
+template <typename T> constexpr int kBlockRows = sizeof(T) == 2 ? kPagedWarpRows : 16;
 constexpr int kRing = 24576;        // bytes of a warp's ring
 constexpr int kMinTiles = 2;        // a range is at least this many tiles
 constexpr int kAngles = 2048;       // bytes of a warp's angle table: the tokens of a query block
@@ -96,6 +96,11 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// a pair of values as bf16 high parts and what they leave, rounded to bf16: 2^-17 of the value
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x, y);
+  lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
 }
 // x = hi + lo with both in tf32 (11 significant bits each): hi hi + hi lo + lo hi leaves out
 // lo lo, 2^-22 of the product, next to fp32's own 2^-24
@@ -199,6 +204,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   using G = Geo<T, D>;
   constexpr int KT = G::KT, RB = G::RB, TILE = G::TILE, NST = G::NST;
   constexpr bool BF = sizeof(T) == 2;
+  // query rows of a block: the MMA's 16, or (bf16) 8 with their high parts as the MMA's rows 0-7
+  // and their low parts as its rows 8-15, so that neither the rotated queries nor the
+  // probabilities lose to bf16 what a single part would (the tensor cores' work is the same, and
+  // decode has few rows)
+  constexpr int kRows = kBlockRows<T>;
+  constexpr int HR = kRows / 8;                  // rows of a lane
   constexpr int NT = D / 8;                      // 8-wide output tiles
   constexpr int KS = BF ? D / 16 : D / 8;        // k steps of the scores
   extern __shared__ __align__(128) unsigned char sm_raw[];
@@ -381,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
     uint32_t qh[KS][4];                       // query fragments (bf16, or tf32 high parts)
     uint32_t ql[BF ? 1 : KS][4];              // fp32: low parts
     float o[NT][4];
-    float m[2], l[2];
+    float m[HR], l[HR];
     int v = 0;
     while (v < n_tiles) {
       // ---- one query block's share of the range
@@ -393,32 +404,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       // own, and the angles of a token are the same for all its heads: the warp computes them
       // once into a table in shared memory, some tokens at a time (the first exactly, the next
       // ones by rotating on: at most 15 steps of 2^-23).
-      int vis[2], row_tok[2];  // last local row that query rows gr and gr + 8 see; their tokens
+      int vis[HR], row_tok[HR];  // last local row that query rows gr (+ 8) see; their tokens
       const int tok0 = cu.blk * kRows / Gq;
       const int n_tok = (cu.blk * kRows + nrow - 1) / Gq - tok0 + 1;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < HR; ++hf) {
         const int row = cu.blk * kRows + min(gr + 8 * hf, nrow - 1);
         const int tok = row / Gq;
         vis[hf] = cu.q.L - cu.q.T + tok;
         row_tok[hf] = tok - tok0;
         const T* src = static_cast<const T*>(p.Q) + (int64_t)(cu.q.a + tok) * p.q_stride +
                        (head * Gq + row % Gq) * D;
-        if constexpr (BF) {  // the values as stored; turned below
 #pragma unroll
-          for (int kk = 0; kk < KS; ++kk)
+        for (int kk = 0; kk < KS; ++kk)  // the values as stored; turned below
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              qh[kk][hf + 2 * e] =
-                  __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + e * 8 + 2 * t4));
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              qh[kk][hf + 2 * e] =
-                  __ldg(reinterpret_cast<const uint32_t*>(src + kk * 8 + e * 4 + t4));
-        }
+          for (int e = 0; e < 2; ++e) {
+            qh[kk][hf + 2 * e] = __ldg(reinterpret_cast<const uint32_t*>(
+                BF ? src + kk * 16 + e * 8 + 2 * t4 : src + kk * 8 + e * 4 + t4));
+            if constexpr (BF) qh[kk][1 + 2 * e] = 0u;  // low parts
+          }
       }
       if (p.rope) {
         constexpr int PL = D / 64;                  // RoPE pairs of a lane: l, l + 32
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
           }
           __syncwarp();
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int hf = 0; hf < HR; ++hf) {
             const int t = row_tok[hf] - t0;
             if (t < 0 || t >= CAP) continue;
             const float2* ang = table + t * (D / 2);
@@ -453,15 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             for (int kk = 0; kk < KS / 2; ++kk) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                uint32_t& lo = qh[kk][hf + 2 * e];
-                uint32_t& hi = qh[kk + KS / 2][hf + 2 * e];
+                uint32_t& lo = qh[kk][hf + 2 * e];           // dims i
+                uint32_t& hi = qh[kk + KS / 2][hf + 2 * e];  // and i + D / 2
                 if constexpr (BF) {
-                  // rounded to bf16 for the tensor cores, as the keys were when appended
                   const float4 c = *reinterpret_cast<const float4*>(ang + kk * 16 + e * 8 + 2 * t4);
                   const float a0 = __uint_as_float(lo << 16), a1 = __uint_as_float(lo & 0xFFFF0000u);
                   const float b0 = __uint_as_float(hi << 16), b1 = __uint_as_float(hi & 0xFFFF0000u);
-                  lo = pack_bf16(a0 * c.x - b0 * c.y, a1 * c.z - b1 * c.w);
-                  hi = pack_bf16(b0 * c.x + a0 * c.y, b1 * c.z + a1 * c.w);
+                  split_bf16(a0 * c.x - b0 * c.y, a1 * c.z - b1 * c.w, lo, qh[kk][1 + 2 * e]);
+                  split_bf16(b0 * c.x + a0 * c.y, b1 * c.z + a1 * c.w, hi,
+                             qh[kk + KS / 2][1 + 2 * e]);
                 } else {
                   const float2 c = ang[kk * 8 + e * 4 + t4];
                   const float a = __uint_as_float(lo), b = __uint_as_float(hi);
@@ -487,8 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < HR; ++hf) {
+        m[hf] = -INFINITY;
+        l[hf] = 0.f;
+      }
       const int first_vis = cu.q.L - cu.q.T + cu.blk * kRows / Gq;  // of the block's first token
 
       for (; cu.t < t_end; ++cu.t, ++v) {
@@ -517,8 +524,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
               mma_bf16(sc[n + 1], qh[kk], b[2], b[3]);
             }
           }
+#pragma unroll
+          for (int n = 0; n < NK; ++n) {  // q_hi k + q_lo k
+            sc[n][0] += sc[n][2];
+            sc[n][1] += sc[n][3];
+          }
         } else {
-          float sl[4] = {0.f, 0.f, 0.f, 0.f};  // the small products apart: two shorter chains
+          // The tensor cores drop bits when they add to a running sum: the small products and
+          // every fourth of the large ones have a sum of their own, added up in fp32.
+          float sl[4] = {0.f, 0.f, 0.f, 0.f}, sh[4][4];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sh[e >> 2][e & 3] = 0.f;
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) {
             uint32_t h0, l0, h1, l1;
@@ -527,24 +543,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             split_tf32(lds32(rowa + (((2 * kk + 1) ^ gr) << 4)), h1, l1);
             mma_tf32(sl, ql[kk], h0, h1);
             mma_tf32(sl, qh[kk], l0, l1);
-            mma_tf32(sc[0], qh[kk], h0, h1);
+            mma_tf32(sh[kk & 3], qh[kk], h0, h1);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[0][e] += sl[e];
+          for (int e = 0; e < 4; ++e)
+            sc[0][e] = ((sh[0][e] + sh[1][e]) + (sh[2][e] + sh[3][e])) + sl[e];
         }
         if (!full) {
 #pragma unroll
           for (int n = 0; n < NK; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2 * HR; ++e) {
               const int key = k0 + n * 8 + 2 * t4 + (e & 1);
               const int lim = ctx ? cu.q.C - 1 : min(vis[e >> 1], cu.q.L - 1);
               if (key > lim) sc[n][e] = -INFINITY;
             }
         }
-        float alpha[2];
+        float alpha[HR];
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < HR; ++hf) {
           float mx = fmaxf(sc[0][2 * hf], sc[0][2 * hf + 1]);
 #pragma unroll
           for (int n = 1; n < NK; ++n) mx = fmaxf(mx, fmaxf(sc[n][2 * hf], sc[n][2 * hf + 1]));
@@ -564,23 +581,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             }
           l[hf] = fmaf(l[hf], alpha[hf], sum);
         }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[HR - 1] != 1.f)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             o[nt][0] *= alpha[0];
             o[nt][1] *= alpha[0];
-            o[nt][2] *= alpha[1];
-            o[nt][3] *= alpha[1];
+            o[nt][2] *= alpha[HR - 1];
+            o[nt][3] *= alpha[HR - 1];
           }
         }
         if constexpr (BF) {
-          // the probabilities enter the product in bf16 (their sum above in fp32)
           const int key = lane & 15;
 #pragma unroll
           for (int n = 0; n < NK; n += 2) {
-            const uint32_t a[4] = {
-                pack_bf16(sc[n][0], sc[n][1]), pack_bf16(sc[n][2], sc[n][3]),
-                pack_bf16(sc[n + 1][0], sc[n + 1][1]), pack_bf16(sc[n + 1][2], sc[n + 1][3])};
+            uint32_t a[4];  // rows 0-7 high parts, 8-15 low parts
+            split_bf16(sc[n][0], sc[n][1], a[0], a[1]);
+            split_bf16(sc[n + 1][0], sc[n + 1][1], a[2], a[3]);
 #pragma unroll
             for (int nn = 0; nn < NT / 2; ++nn) {
               uint32_t b[4];
@@ -603,16 +619,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             const uint32_t ch = 2 * nt + (gr >> 2), in = (gr & 3) * 4;
             split_tf32(lds32(vb + (2 * t4) * RB + ((ch ^ (2 * t4)) << 4) + in), h0, l0);
             split_tf32(lds32(vb + (2 * t4 + 1) * RB + ((ch ^ (2 * t4 + 1)) << 4) + in), h1, l1);
-            mma_tf32(o[nt], al, h0, h1);
-            mma_tf32(o[nt], ah, l0, l1);
-            mma_tf32(o[nt], ah, h0, h1);
+            float d[4] = {0.f, 0.f, 0.f, 0.f};  // (added to the running sum in fp32)
+            mma_tf32(d, al, h0, h1);
+            mma_tf32(d, ah, l0, l1);
+            mma_tf32(d, ah, h0, h1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][e] += d[e];
           }
         }
       }
 
       // ---- the block's rows, or this range's partial of them
+      if constexpr (BF) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+        for (int nt = 0; nt < NT; ++nt) {  // p_hi v + p_lo v
+          o[nt][0] += o[nt][2];
+          o[nt][1] += o[nt][3];
+        }
+      }
+#pragma unroll
+      for (int hf = 0; hf < HR; ++hf) {
         l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
         l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
         const int lr = gr + 8 * hf;
@@ -757,6 +783,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) paged_merge_kernel(PagedAtte
                                                                        int tc_grid, int n_cta) {
   constexpr int EL = D / 32;  // elements a lane holds
   constexpr int W = kMergeThreads / 32;
+  constexpr int kRows = kBlockRows<T>;
   __shared__ float sh_o[W][D];
   __shared__ float sh_m[W], sh_l[W];
   // blocks of few and of many segments: which range, first row task, how many rows
@@ -982,15 +1009,15 @@ PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int
   // one CTA per SM; more when the heads alone need more warps
   pl.grid = std::max(sms, (h_kv + pga::kWarps - 1) / pga::kWarps);
   pl.S = pl.grid * pga::kWarps / h_kv;
-  // The tcgen05 kernel serves the bf16 requests with more than 16 query rows per KV head. The
+  // The tcgen05 kernel serves the bf16 requests with more than 8 query rows per KV head. The
   // host sees only the totals: it leaves the launch out where no request can have so many, and
   // where there is at most one new token per request on average (a decode step, where the launch
   // would cost its latency and find nothing; the warp-level kernel serves a longer request too).
   const int Gq = h_q / h_kv;
   const bool tc = dtype == 1 && Gq <= 256 && (int64_t)n_rows * Gq > kPagedWarpRows &&
-                  n_rows > n_req;
+                  (n_rows > n_req || Gq > kPagedWarpRows);
   pl.tc_grid = tc ? sms : 0;
-  const size_t slots = (size_t)pl.S * 2 * h_kv * pga::kRows;
+  const size_t slots = (size_t)pl.S * 2 * h_kv * (dtype == 1 ? kPagedWarpRows : 16);
   pl.err_bytes = al((size_t)(pl.grid + pl.tc_grid) * sizeof(int));
   pl.tail_bytes = al((size_t)pl.S * sizeof(int4));
   pl.ml_bytes = al(slots * 2 * sizeof(float));
