@@ -405,7 +405,8 @@ struct PagedAttendParams {
   int4* tc_tail;            // [tc_grid][2]
   float* tc_ml;             // [tc_grid][2][256][2] its partials
   float* tc_o;              // [tc_grid][2][256][d]
-  __nv_bfloat16* q_rot;     // [h_kv][d / 64][n_rows * h_q / h_kv][64] its rotated queries
+  __nv_bfloat16* q_rot;     // [2][h_kv][d / 64][n_rows * h_q / h_kv][64] its rotated queries
+                            // (high and low parts)
 };
 struct PagedPlan {
   int grid, S;              // CTAs; ranges that the tile list is cut into (per KV head)

@@ -128,7 +128,8 @@ __device__ __forceinline__ int range_of(int64_t y, int64_t x, int S) {
 // its operand layout: per KV head and 64 dims the rows (token, query head of the group) one after
 // another, 16-byte chunk c of a row at c ^ (row within its block & 7). A warp takes 16 heads of a
 // token (their loads in flight together): its angles once into the warp's table, then a lane one
-// 16-byte chunk of the lower half of a head and its partner half a head on.
+// 16-byte chunk of the lower half of a head and its partner half a head on. What rounding to bf16
+// leaves follows in a second copy, for the blocks that take it.
 template <int D>
 __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w, int n_warps,
                                                int lane, float2* table,
@@ -170,6 +171,7 @@ __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w
 #pragma unroll
     for (int e = 0; e < 4; ++e) cs[e] = *reinterpret_cast<const float4*>(table + c * 8 + 2 * e);
     const int x0 = (t % TB) * Gq;
+    const bool low = min(TB, q.T - t / TB * TB) * Gq <= 128;  // a block of one half
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
       const int h = h0 + k * HPW;
@@ -178,22 +180,27 @@ __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w
       float a[8], b[8];
       V::unpack(ra[k], a);
       V::unpack(rb[k], b);
-      uint32_t oa[4], ob[4];
+      uint32_t oa[4], ob[4], la[4], lb[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        oa[e] = pack_bf16(a[2 * e] * cs[e].x - b[2 * e] * cs[e].y,
-                          a[2 * e + 1] * cs[e].z - b[2 * e + 1] * cs[e].w);
-        ob[e] = pack_bf16(b[2 * e] * cs[e].x + a[2 * e] * cs[e].y,
-                          b[2 * e + 1] * cs[e].z + a[2 * e + 1] * cs[e].w);
+        split_bf16(a[2 * e] * cs[e].x - b[2 * e] * cs[e].y,
+                   a[2 * e + 1] * cs[e].z - b[2 * e + 1] * cs[e].w, oa[e], la[e]);
+        split_bf16(b[2 * e] * cs[e].x + a[2 * e] * cs[e].y,
+                   b[2 * e + 1] * cs[e].z + a[2 * e + 1] * cs[e].w, ob[e], lb[e]);
       }
       const int kv = h / Gq, g = h % Gq;
       const int x = (x0 + g) & 7;
       __nv_bfloat16* dst =
           p.q_rot + ((int64_t)kv * (D / 64) * rows + (int64_t)i * Gq + g) * 64;
-      *reinterpret_cast<uint4*>(dst + ((c ^ x) << 3)) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
       const int cb = c + HC;  // D = 64: the same 64 dims; D = 128: the next ones
-      *reinterpret_cast<uint4*>(dst + (cb >> 3) * rows * 64 + (((cb & 7) ^ x) << 3)) =
-          make_uint4(ob[0], ob[1], ob[2], ob[3]);
+      const int64_t oa_at = (c ^ x) << 3, ob_at = (cb >> 3) * rows * 64 + (((cb & 7) ^ x) << 3);
+      *reinterpret_cast<uint4*>(dst + oa_at) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+      *reinterpret_cast<uint4*>(dst + ob_at) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+      if (low) {
+        dst += (int64_t)p.h_q * p.n_rows * D;
+        *reinterpret_cast<uint4*>(dst + oa_at) = make_uint4(la[0], la[1], la[2], la[3]);
+        *reinterpret_cast<uint4*>(dst + ob_at) = make_uint4(lb[0], lb[1], lb[2], lb[3]);
+      }
     }
     __syncwarp();  // the table is filled anew
   }
@@ -1025,7 +1032,7 @@ PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int
   pl.tc_tail_bytes = al((size_t)pl.tc_grid * 2 * sizeof(int4));
   pl.tc_ml_bytes = al((size_t)pl.tc_grid * 2 * 256 * 2 * sizeof(float));
   pl.tc_o_bytes = al((size_t)pl.tc_grid * 2 * 256 * d * sizeof(float));
-  pl.q_bytes = tc ? al((size_t)n_rows * h_q * d * 2) : 0;
+  pl.q_bytes = tc ? al((size_t)n_rows * h_q * d * 2 * 2) : 0;
   pl.smem = pga::kWarps * (pga::kRing + pga::kAngles) +
             (n_req <= pga::kReqCache
                  ? (pga::kReqCache + 4) * sizeof(int32_t) + pga::kReqCache * sizeof(int4)

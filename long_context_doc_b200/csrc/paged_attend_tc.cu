@@ -449,7 +449,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         return true;
       };
       bool ok = true;
-      uint32_t nq[2] = {0, 0};
+      uint32_t n_blk[2] = {0, 0};  // blocks whose queries each half's barrier has seen
+      bool was_two = false;
       // the rotated queries are written by the grid launched before this one
       asm volatile("griddepcontrol.wait;" ::: "memory");
       while (ok) {
@@ -464,26 +465,36 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         ++nb;
         ok = uniform(ok) != 0;
         if (!ok) break;
-        // the block's queries: a half's rows are consecutive in each slice of its head's
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int rows = min(w.rows - h * kHalf, kHalf);
-          if (rows <= 0) continue;
-          if (lane == 0 && nq[h] > 0)
-            ok = ok && wait_or_abort(&qempty[h], (nq[h] - 1) & 1, &cta_err, abort_flag);
-          ok = uniform(ok) != 0;
-          if (!ok) break;
-          ++nq[h];
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&qfull[h], (uint32_t)(rows * 128 * SL));
+        // the block's queries, once the scores of the block before are formed: a half's rows are
+        // consecutive in each slice of its head's; one half's low parts take the other's place
+        const bool two = w.rows > kHalf;
+        if (lane == 0) {
+          if (n_blk[0] > 0) ok = wait_or_abort(&qempty[0], (n_blk[0] - 1) & 1, &cta_err, abort_flag);
+          if (was_two)
+            ok = ok && wait_or_abort(&qempty[1], (n_blk[1] - 1) & 1, &cta_err, abort_flag);
+        }
+        ok = uniform(ok) != 0;
+        if (!ok) break;
+        was_two = two;
+        ++n_blk[0];
+        n_blk[1] += two;
+        if (lane == 0) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int rows = two ? min(w.rows - h * kHalf, kHalf) : w.rows;
+            uint64_t* bar = &qfull[two ? h : 0];
+            if (two || h == 0)
+              mbar_arrive_expect_tx(bar, (uint32_t)(rows * 128 * SL) * (two ? 1u : 2u));
             for (int sl = 0; sl < SL; ++sl)
               bulk_g2s(q_s + h * C::kTile + sl * kSlice,
-                       p.q_rot + (((int64_t)w.head * SL + sl) * p.n_rows * Gq +
-                                  (int64_t)(w.q.a + w.blk * walk.TB) * Gq + h * kHalf) * 64,
-                       (uint32_t)rows * 128u, &qfull[h]);
+                       p.q_rot + (((int64_t)((two ? 0 : h * p.h_kv) + w.head) * SL + sl) *
+                                      p.n_rows * Gq +
+                                  (int64_t)(w.q.a + w.blk * walk.TB) * Gq + (two ? h * kHalf : 0)) *
+                                     64,
+                       (uint32_t)rows * 128u, bar);
           }
-          __syncwarp();
         }
+        __syncwarp();
         // K0 K1 V0 K2 V1 .. : a tile's V is needed a softmax after its K, and in a slot it takes up
         // from its copy's issue on
         Piece last{};
@@ -519,7 +530,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       }
       // the copies issued land before the CTA can exit
       for (int h = 0; h < 2; ++h)
-        if (nq[h] > 0) mbar_wait_bounded(&qfull[h], (nq[h] - 1) & 1, &cta_err);
+        if (n_blk[h] > 0) mbar_wait_bounded(&qfull[h], (n_blk[h] - 1) & 1, &cta_err);
       for (uint32_t q = seq > NS ? seq - NS : 0; q < seq; ++q)
         mbar_wait_bounded(&full[q % NS], (q / NS) & 1, &cta_err);
     } else if (warp == 1) {
@@ -536,13 +547,21 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         return uniform(wait_or_abort(bar, par, &cta_err, abort_flag)) != 0;
       };
       auto wait_ring = [&](uint32_t q) { return wait(&full[q % NS], (q / NS) & 1); };
-      auto scores = [&](int h, int slot, int bar, int st) {  // S[slot] = Q_h K^T
+      // (low: with the queries' low parts)
+      auto scores = [&](int h, int slot, int bar, int st, bool low) {  // S[slot] = Q_h K^T
         fence_after();
         const uint64_t a = q_desc + h * kStep, b = k_desc + st * kStep;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {  // 16 dims a step: 32 bytes of a row, 64 dims a slice
           const uint32_t off = (kk >> 2) * (kSlice >> 4) + 2 * (kk & 3);
           mma_ss(tmem + slot * 128, a + off, b + off, idesc_s, kk ? 1u : 0u);
+        }
+        if (low) {
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+            const uint32_t off = (kk >> 2) * (kSlice >> 4) + 2 * (kk & 3);
+            mma_ss(tmem + slot * 128, a + kStep + off, b + off, idesc_s, 1u);
+          }
         }
         commit(&sfull[bar]);
       };
@@ -575,7 +594,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           for (int h = 0; h < 2; ++h) {
             ok = ok && wait(&qfull[h], nq[h] & 1);
             ++nq[h];
-            if (ok) scores(h, h, h, seq % NS);
+            if (ok) scores(h, h, h, seq % NS, false);
             if (ok && n == 1) commit(&qempty[h]);
           }
           if (!ok) break;
@@ -592,7 +611,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             if (last) {
               commit(&odone[0]);
             } else {
-              scores(0, 0, 0, k % NS);
+              scores(0, 0, 0, k % NS, false);
               if (j + 2 == n) commit(&qempty[0]);
             }
             ok = product(1, 1, 1, np[1] & 1, v % NS, j == 0);
@@ -602,7 +621,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             if (last) {
               commit(&odone[1]);
             } else {
-              scores(1, 1, 1, k % NS);
+              scores(1, 1, 1, k % NS, false);
               if (j + 2 == n) commit(&qempty[1]);
               commit(&empty[k % NS]);
             }
@@ -612,7 +631,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           ok = wait_ring(seq) && wait(&qfull[0], nq[0] & 1);
           ++nq[0];
           if (!ok) break;
-          scores(0, 0, 0, seq % NS);
+          scores(0, 0, 0, seq % NS, true);
           if (n == 1) commit(&qempty[0]);
           commit(&empty[seq % NS]);
 #pragma unroll 1
@@ -623,7 +642,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             if (!last) {
               ok = wait_ring(k);
               if (!ok) break;
-              scores(0, slot ^ 1, slot ? 0 : 2, k % NS);
+              scores(0, slot ^ 1, slot ? 0 : 2, k % NS, true);
               if (j + 2 == n) commit(&qempty[0]);
               commit(&empty[k % NS]);
             }
