@@ -1,8 +1,10 @@
 """The paged local context (page_plan, paged_append, paged_attend) against plain 64-bit forms.
 
 Tolerances follow from the roundings, element by element. bf16 (half a step 2^-8): the rotated
-query is rounded, so a score moves by at most 2^-8 scale sum|q k| = ds and a probability by a
-factor within exp(2 ds); the probabilities are rounded (2^-8) and so is the output (2^-8 |o|).
+query may be rounded, so a score moves by at most 2^-8 scale sum|q k| = ds and a probability by a
+factor within exp(2 ds); the probabilities may be rounded (2^-8) and the output is (2^-8 |o|).
+Where both enter the products with their low parts (eight query rows per KV head or fewer),
+test_decode_keeps_the_low_parts holds them to 2^-16 instead.
 fp32: products of tf32 high and low parts leave out 2^-22 of each product (the low parts'
 rounding twice, and low x low), the tensor core's accumulation may drop 2^-22 of the running sum a
 step; the score, the probabilities' exponential (2^-22) and the product with V err accordingly.
@@ -545,6 +547,12 @@ ATTEND = {
                          64, 32, 8, 128, [i % 5 * 8 for i in range(24)]),
     "halves_alternate_d64": ([700 + 61 * i for i in range(20)],
                              [(3, 70, 5, 40)[i % 4] for i in range(20)], 16, 32, 4, 64, None),
+    "five_heads_chunk": ([333, 12], [200, 12], 32, 10, 2, 128, [7, 0]),
+    "hundred_heads": ([150, 40], [5, 1], 16, 200, 2, 64, [0, 9]),
+    "past_a_block_of_heads": ([70, 33], [2, 1], 16, 300, 1, 64, [3, 0]),
+    "sixteen_heads_decode": ([700, 90, 1], [1, 1, 1], 16, 32, 2, 128, [5, 0, 0]),
+    "long_chunk": ([5000], [700], 64, 8, 2, 128, [100]),
+    "chunk_longer_than_context": ([100, 0], [300, 40], 16, 8, 2, 128, [9, 0]),
     "many_kv_heads": ([40, 9], [2, 1], 16, 24, 12, 64, [3, 0]),
 }
 
@@ -597,6 +605,39 @@ def test_attend_equal_and_extreme_scores(msa, gpu):
         c.K[page, row] = 100.0 * torch.sign(c.Q[0, 0])
         c.k64[0][19] = 100.0 * np.sign(c.q64[0, 0])
         c.check(c.run(msa))
+
+
+@gpu_test
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,T,h_q,h_kv", [([3000, 17, 900], 1, 8, 2), ([65], 4, 4, 2),
+                                             ([40, 2500], 1, 5, 5)])
+def test_decode_keeps_the_low_parts(msa, gpu, lens, T, h_q, h_kv, d):
+    """Eight query rows per KV head or fewer: queries and probabilities are high and low bf16
+    parts, which leave 2^-16 of a value (two half steps); the output's rounding is the rest."""
+    c = Case(gpu, 17, "bf16", lens, [T] * len(lens), 16, h_q, h_kv, d, [5] * len(lens))
+    got = c.run(msa)[:c.rows].double().cpu().numpy()
+    g = h_q // h_kv
+    a = 0
+    for r, L in enumerate(lens):
+        local = L - T + np.arange(T)
+        q = rotate64(c.q64[a:a + T], c.pos0 + local)
+        for h in range(h_q):
+            k = np.concatenate([c.ck64[r, :5, h // g], c.k64[r][:, h // g]])
+            v = np.concatenate([c.cv64[r, :5, h // g], c.v64[r][:, h // g]])
+            for t in range(T):
+                n = 5 + local[t] + 1
+                s = k[:n] @ q[t, h] * d ** -0.5
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                o = p @ v[:n]
+                # 2^-16 of the score's terms for the query's parts, as much for the angles'
+                # and the fp32 sums' errors (2^-18 and n d 2^-24 at most), 2^-16 of the
+                # probabilities twice (their parts; exponential and sums)
+                ds = 2.0 ** -15 * (np.abs(k[:n]) @ np.abs(q[t, h])).max() * d ** -0.5
+                tol = (math.expm1(2 * ds) + 2 * 2.0 ** -16) * (p @ np.abs(v[:n])) + \
+                    2.0 ** -8 * np.abs(o)
+                assert (np.abs(got[a + t, h] - o) <= tol).all(), (r, h, t)
+        a += T
 
 
 @gpu_test
