@@ -181,7 +181,8 @@ struct Work {
   int r, head, blk, nb, CT;
   int t0, t1;        // this CTA's tiles of the block, of n_tiles
   int n_tiles;
-  int rows;          // query rows of the block
+  int toks, rows;    // tokens and query rows of the block
+  int first;         // local row of its first token
   int more;          // the share goes on after it
 };
 struct Share {
@@ -226,7 +227,9 @@ struct Walk {
   }
   __device__ __forceinline__ void set(Work& w, int from) {
     w.n_tiles = tiles(w.q, w.blk);
-    w.rows = min(TB, w.q.T - w.blk * TB) * Gq;
+    w.toks = min(TB, w.q.T - w.blk * TB);
+    w.rows = w.toks * Gq;
+    w.first = w.q.L - w.q.T + w.blk * TB;
     w.t0 = from;
     w.t1 = min(w.n_tiles, from + left);
     left -= w.t1 - from;
@@ -668,6 +671,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t o_col = lane_base + 256 + h * 128;
       const float c = p.scale_log2;
+      const int row = h * kHalf + lrow, row_tok = row / Gq;  // row of a block, its token
       uint32_t n_own = 0, n_alt = 0;  // phases of sfull[h], of sfull[2]
       uint32_t no = 0, npd = 0;       // of odone[h], of pdone
       uint32_t seq = 0;            // ring tile of the block's first K
@@ -688,10 +692,9 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         const bool any_row = h * kHalf + (warp & 3) * 32 < w.rows;  // of the warp
         float m = -INFINITY, l = 0.f;
         if (active) {
-          const int row = h * kHalf + lrow;
           // last visible local row of this row and of the half's first
-          const int vis = n_loc - w.q.T + w.blk * walk.TB + min(row, w.rows - 1) / Gq;
-          const int vis_first = min(n_loc - w.q.T + w.blk * walk.TB + h * kHalf / Gq, n_loc - 1);
+          const int vis = w.first + min(row_tok, w.toks - 1);
+          const int vis_first = min(w.first + h * (walk.TB >> 1), n_loc - 1);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           for (int t = t0; t < t1; ++t) {
             const bool ctx = t < CT;
@@ -807,37 +810,36 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           ok = wait(&odone[h], no++ & 1);
           if (!ok) break;
           fence_after();
-          const int row = h * kHalf + lrow;
           const bool whole = begins && ends;
           // A lane holds a row: its 128-byte pieces go through shared memory (16-byte chunk c of
           // row r at c ^ (r & 7)), so that eight lanes write a piece of one row together.
           if (any_row) {
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int64_t pslot =
-                ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf) + row;
-            const int tok = w.blk * walk.TB + row / Gq;
+            const int64_t pslot = ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (2 * kHalf);
             unsigned char* dst =
                 whole ? reinterpret_cast<unsigned char*>(
                             static_cast<__nv_bfloat16*>(p.O) +
-                            ((int64_t)(w.q.a + tok) * p.h_q + w.head * Gq + row % Gq) * D)
+                            ((int64_t)(w.q.a + w.blk * walk.TB) * p.h_q + w.head * Gq) * D)
                       : reinterpret_cast<unsigned char*>(p.tc_o + pslot * D);
+            dst += (lane & 7) * 16;
+            // the row's place: query head row - row_tok Gq of its group, or a row of the partial
+            const uint32_t off = whole ? (uint32_t)((row_tok * (p.h_q - Gq) + row) * D * 2)
+                                       : (uint32_t)(row * D * 4);
             unsigned char* mine = bounce + (warp - 2) * kBounce;
             const int n_row = w.rows - (row - lane);             // the warp's rows
             const int steps = whole ? D / 64 : D / 32;
 #pragma unroll 1
-            for (int st = 0; st < steps; ++st) {
+            for (int st = 0; st < steps; ++st, dst += 128) {
               uint32_t ov[32];
               if (whole) {
+                uint32_t f[64];
+                ld32(o_col + st * 64, f);
+                ld32(o_col + st * 64 + 32, f + 32);
+                wait_ld();
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                  uint32_t f[32];
-                  ld32(o_col + st * 64 + hf * 32, f);
-                  wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    ov[hf * 16 + i] = pack_bf16(__uint_as_float(f[2 * i]) * inv,
-                                                __uint_as_float(f[2 * i + 1]) * inv);
-                }
+                for (int i = 0; i < 32; ++i)
+                  ov[i] = pack_bf16(__uint_as_float(f[2 * i]) * inv,
+                                    __uint_as_float(f[2 * i + 1]) * inv);
               } else {
                 ld32(o_col + st * 32, ov);
                 wait_ld();
@@ -847,19 +849,23 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                 *reinterpret_cast<uint4*>(mine + lane * 128 + ((i ^ (lane & 7)) << 4)) =
                     make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
               __syncwarp();
+              uint4 v[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const int r = i * 4 + (lane >> 3);
-                unsigned char* to = reinterpret_cast<unsigned char*>(__shfl_sync(
-                    0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
-                const uint4 v = *reinterpret_cast<const uint4*>(mine + r * 128 +
-                                                                (((lane & 7) ^ (r & 7)) << 4));
-                if (r < n_row) *reinterpret_cast<uint4*>(to + st * 128 + (lane & 7) * 16) = v;
+                v[i] = *reinterpret_cast<const uint4*>(mine + r * 128 +
+                                                       (((lane & 7) ^ (r & 7)) << 4));
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3);
+                const uint32_t to = __shfl_sync(0xffffffffu, off, r);
+                if (r < n_row) *reinterpret_cast<uint4*>(dst + to) = v[i];
               }
               __syncwarp();
             }
             if (!whole && lane < n_row)
-              *reinterpret_cast<float2*>(p.tc_ml + pslot * 2) = make_float2(m, l);
+              *reinterpret_cast<float2*>(p.tc_ml + (pslot + row) * 2) = make_float2(m, l);
           }
           fence_before();  // O is read before the next block's products
         }
