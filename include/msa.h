@@ -468,8 +468,9 @@ msa_status msa_encode_hidden(const void* H, int64_t n_tok, int32_t D, const void
  * row_start[r] .. row_start[r + 1] are request r's. All lengths, counts and tables are int32 in
  * device memory, so a captured step replays with the current ones; rows behind the last
  * request's (padding) are neither read nor written.
- * Limits: page_size a power of two from 16 to 2^20, n_req <= 4096, the pool and a request up to
- * 2^31 - 1 rows, h_kv <= 1024.
+ * Limits: page_size a power of two from 16 to 2^20, n_req <= 4096, a pool of up to 2^31 - 1 and
+ * a request of up to 2^30 rows, h_kv <= 1024. Requests may share pages that none of them appends
+ * to.
  */
 
 /* msa_page_plan - block tables and slot maps of a step from the requests' lengths.
@@ -509,8 +510,8 @@ msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
  * (rope_base <= 0: as given), V_pages[slot_map[i]] <- V_new[i], for the n_rows rows of a step
  * (K before RoPE, like K_loc); rows with a negative slot are skipped. K_new, V_new: n_rows rows
  * of [h_kv, d], k_stride / v_stride elements apart (for slices of a fused projection; multiples
- * of 16 bytes). Slots are distinct (of rows with one slot, any may stay). A slot past the pool
- * is skipped and recorded in the status word of ws (>= 256 bytes, 256-byte aligned), which this
+ * of 16 bytes). Slots are distinct (rows with one slot leave a mix of them there), and the pools
+ * do not overlap the inputs. A slot past the pool is skipped and recorded in the status word of ws (>= 256 bytes, 256-byte aligned), which this
  * call only ever sets: give it the plan's workspace, which msa_page_plan starts every step, or
  * one that the caller zeroes. */
 msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
@@ -533,12 +534,18 @@ msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32
  *            (max_ctx = 0: none, the three may be NULL).
  * O          [n_rows, h_q, d]: softmax over {memory rows < ctx_len[r]} U {local rows <= the
  *            token's own} of scale * q.k (scale <= 0: 1/sqrt(d)), times V; 0 for a token that
- *            sees nothing. fp32 accumulation and softmax; bf16 inputs enter the tensor cores
- *            with the rotated query and the probabilities rounded to bf16.
+ *            sees nothing. O overlaps no input. fp32 accumulation and softmax. bf16: up to eight
+ *            query rows per KV head (T * h_q / h_kv) enter the tensor cores with the rotated
+ *            query and the probabilities as high and low bf16 parts (the output's rounding is
+ *            what is left), more rows with the probabilities, blocks of more than 128 with the
+ *            rotated query too, rounded to bf16. fp32: products of tf32 high
+ *            and low parts (2^-22).
  * Rows of the request that a token does not see are given weight 0 exactly, but they are read
  * with the tile they share with visible ones: their V must be finite.
  * A request whose length, row starts or pages are out of range is recorded in the status word
- * (3); its rows of O are unspecified or not written, other requests' are right.
+ * (3); its rows of O are unspecified or not written, other requests' are right as long as no rows
+ * are claimed twice. Status 1: a device wait expired; 2: more than 2^31 tiles of work (nothing
+ * is computed).
  * ws         msa_paged_attend_workspace(...) bytes, 256-byte aligned, not shared with a call
  *            that runs at the same time. The result does not depend on its contents.
  */

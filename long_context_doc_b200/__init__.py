@@ -681,12 +681,14 @@ def _explain_pool(what: str, K_pages, V_pages):
 
 def _launch(dev: int, stream, f, *args):
     """f(*args, stream) with device ``dev`` current, on ``stream`` or the device's current one."""
+    if dev < 0:
+        raise MSAError(1, "the tensors are not in device memory")
     if stream is None:
         # the raw handle of torch.cuda.current_stream(dev), at a twentieth of its 3 us
-        stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+        stream = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if dev < 0 or torch.cuda.current_device() == dev:
+    if torch.cuda.current_device() == dev:
         status = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -767,8 +769,9 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
     n_pages, page = K_pages.shape[:2]
     _launch(dev, stream, lib.msa_paged_append, K_pages.data_ptr(), V_pages.data_ptr(), n_pages,
             page, slot_map.data_ptr(), row_pos.data_ptr(), K_new.data_ptr(), V_new.data_ptr(),
-            K_new.stride(0), V_new.stride(0), n_rows, h_kv, d, dtype_code(K_pages), pos0,
-            rope_base, ws.data_ptr(), ws.nbytes)
+            K_new.stride(0) if n_rows > 1 else h_kv * d,
+            V_new.stride(0) if n_rows > 1 else h_kv * d, n_rows, h_kv, d, dtype_code(K_pages),
+            pos0, rope_base, ws.data_ptr(), ws.nbytes)
     return ws
 
 
@@ -823,7 +826,8 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
         mem = (None, None, None)
     else:
         mem = (ctxK.data_ptr(), ctxV.data_ptr(), ctx_len.data_ptr())
-    _launch(dev, stream, lib.msa_paged_attend, Q.data_ptr(), Q.stride(0), n_rows, h_q,
+    _launch(dev, stream, lib.msa_paged_attend, Q.data_ptr(),
+            Q.stride(0) if n_rows > 1 else h_q * d, n_rows, h_q,
             row_start.data_ptr(), length.data_ptr(), n_req, K_pages.data_ptr(),
             V_pages.data_ptr(), n_pages, page, block_table.data_ptr(), max_pages, *mem, max_ctx,
             h_kv, d, dtype_code(Q), pos0, rope_base, scale, O.data_ptr(), ws.data_ptr(),
@@ -854,7 +858,7 @@ class PagedCache:
         self.length, self.n_free = self.out["length"], self.out["n_free"]
         self.ws = torch.zeros(max(256, msa_page_plan_workspace(n_req, max_rows)),
                               dtype=torch.uint8, device=device)
-        self._attend_ws = None
+        self._attend_ws = []  # all kept: a captured step goes on using the one it was given
 
     def plan(self, target, stream=None) -> dict:
         """Moves every request to its target length (int32 [n_req], device memory) and returns
@@ -877,9 +881,9 @@ class PagedCache:
                                               self.K.shape[4], dtype_code(self.K),
                                               0 if ctxK is None else ctxK.shape[1], max_pages,
                                               self.page_size)
-            if self._attend_ws is None or self._attend_ws.numel() < need:
-                self._attend_ws = _ws(need, self.K.device)
-            ws = self._attend_ws
+            if not self._attend_ws or self._attend_ws[-1].numel() < need:
+                self._attend_ws.append(_ws(need, self.K.device))
+            ws = self._attend_ws[-1]
         return paged_attend(Q, self.out["row_start"], self.length, self.K[layer], self.V[layer],
                             self.block_table, self.pos0, self.rope_base, ctxK, ctxV, ctx_len,
                             scale, O, ws, stream)

@@ -59,8 +59,8 @@ msa_status check_pool(int32_t page_size, int32_t n_pages, int32_t max_pages, int
           MSA_ERR_UNSUPPORTED, "page size %d (a power of two from %d to 2^20)", page_size, kMinPage);
   REQUIRE(n_pages >= 1 && (int64_t)n_pages * page_size < (1ll << 31), MSA_ERR_INVALID_ARG,
           "n_pages %d (the pool holds 1 to 2^31 - 1 rows)", n_pages);
-  REQUIRE(max_pages >= 1 && (int64_t)max_pages * page_size < (1ll << 31), MSA_ERR_INVALID_ARG,
-          "max_pages %d (a request holds up to 2^31 - 1 rows)", max_pages);
+  REQUIRE(max_pages >= 1 && (int64_t)max_pages * page_size <= (1ll << 30), MSA_ERR_INVALID_ARG,
+          "max_pages %d (a request holds up to 2^30 rows)", max_pages);
   REQUIRE(n_req >= 0, MSA_ERR_INVALID_ARG, "n_req %d", n_req);
   REQUIRE(n_req <= msa::kPagedMaxReq, MSA_ERR_UNSUPPORTED, "n_req %d (up to %d)", n_req,
           msa::kPagedMaxReq);

@@ -316,6 +316,14 @@ def test_helpers_refuse_what_pointers_cannot_show(msa):
         msa.paged_attend(torch.zeros(5, 4, 128), i32(3), i32(2), pool, pool, i32(2, 3), 0, 0.0)
     with pytest.raises(msa.MSAError, match="O is not like Q"):
         msa.paged_attend(Q, i32(3), i32(2), pool, pool, i32(2, 3), 0, 0.0, O=torch.zeros(4, 4, 64))
+    # nothing wrong but where they are
+    with pytest.raises(msa.MSAError, match="device memory"):
+        msa.page_plan(i32(2), i32(2), i32(1), i32(2, 3), i32(4), 16, 8)
+    with pytest.raises(msa.MSAError, match="device memory"):
+        msa.paged_append(pool, pool, i32(3), i32(3), torch.zeros(3, 2, 64),
+                         torch.zeros(3, 2, 64), 0, 0.0)
+    with pytest.raises(msa.MSAError, match="device memory"):
+        msa.paged_attend(Q, i32(3), i32(2), pool, pool, i32(2, 3), 0, 0.0)
 
 
 # ------------------------------------------------------------------ plan
@@ -584,7 +592,7 @@ def test_attend_arguments(msa, gpu, dtype, kw):
 
 
 @gpu_test
-@pytest.mark.parametrize("n", [200, 1000])
+@pytest.mark.parametrize("n", [200, 1000, 4096])
 def test_attend_many_requests(msa, gpu, n):
     rs = np.random.RandomState(n)
     lens = rs.randint(0, 60, n).tolist()
@@ -710,6 +718,47 @@ def test_attend_rows_of_a_long_pool(msa, gpu):
     msa.paged_append(K, V, slot, _i32([0], gpu), new, new, 0, 0.0)
     assert (V[-1, -1] == 1).all() and (K[-1, -1] == 1).all()
     assert int((V[:10].float() != 0).sum()) == 0
+
+
+@gpu_test
+def test_one_row_of_any_stride(msa, gpu):
+    """A single row's stride means nothing (torch leaves it as it was)."""
+    c = Case(gpu, 61, "bf16", [50], [1], 16, 8, 2, 128, None, pad=0)
+    for stride in (1, 7):
+        q = torch.as_strided(c.Q.contiguous(), c.Q.shape, (stride, 128, 1))
+        O = msa.paged_attend(q, c.row_start, c.length, c.K, c.V, c.table, c.pos0, c.base)
+        c.check(O)
+        new = torch.as_strided(torch.ones(1, 2, 128, dtype=torch.bfloat16, device=gpu), (1, 2, 128),
+                               (stride, 128, 1))
+        K = torch.zeros(1, 16, 2, 128, dtype=torch.bfloat16, device=gpu)
+        V = torch.zeros_like(K)
+        msa.paged_append(K, V, _i32([3], gpu), _i32([0], gpu), new, new, 0, 0.0)
+        assert (V[0, 3] == 1).all() and float(V.float().sum()) == 256
+
+
+@gpu_test
+def test_cache_keeps_a_captured_workspace(msa, gpu):
+    """A later, larger call of the cache's own workspace leaves a captured step's alone."""
+    rs = np.random.RandomState(3)
+    f = lambda *s: torch.from_numpy(rs.standard_normal(s).astype(np.float32)).bfloat16().to(gpu)
+    cache = msa.PagedCache(2, 40, 16, 20, 256, 2, 128, rope_base=BASE, device=gpu)
+    cache.plan(_i32([200, 30], gpu))
+    cache.append(0, f(230, 2, 128), f(230, 2, 128))
+    cache.plan(_i32([201, 31], gpu))
+    cache.append(0, f(2, 2, 128), f(2, 2, 128))
+    q = f(2, 4, 128)
+    want = cache.attend(0, q).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cache.attend(0, q)
+    wide = cache.attend(0, f(200, 32, 128), O=torch.zeros(200, 32, 128, dtype=torch.bfloat16,
+                                                          device=gpu))  # a larger workspace
+    junk = [torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device=gpu) for _ in range(8)]
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all(int(j.min()) == 0xFF for j in junk)
+    assert wide.shape == (200, 32, 128)
 
 
 # ------------------------------------------------------------------ the three together
