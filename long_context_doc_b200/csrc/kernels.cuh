@@ -340,6 +340,24 @@ inline cudaError_t allow_smem_once(const void* kernel, size_t bytes,
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
+// Launch whose CTAs may be set up while the kernel before it in the stream ends (programmatic
+// dependent launch). The kernel waits (griddepcontrol.wait) before it touches memory, and lets its
+// own dependents start only after that, so that a chain of such launches stays in order.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 constexpr int kPagedMaxReq = 4096;  // requests of one call (their prefix sums fit shared memory)
 struct PagePlanParams {
   const int32_t* target;   // [n_req] lengths wanted

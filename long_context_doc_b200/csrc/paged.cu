@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "paged.cuh"
 
 namespace msa {
 namespace pgd {
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PagePlanPara
   const int sh = p.page_shift;
   const int pm = (1 << sh) - 1;
   const long long cap = (long long)p.max_pages << sh;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_then_let_start();
 
   if (tid == 0) bad_len = 0;
   const int F = *p.nfree_in;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(PagePlanPara
 }
 
 __global__ void __launch_bounds__(kFillThreads) page_fill_kernel(PagePlanParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_then_let_start();
   const PlanHead h = *reinterpret_cast<const PlanHead*>(p.sums);
   const int32_t* a = p.sums + 4;
   const int n = p.n_req;
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendParams p) 
 #pragma unroll
   for (int e = 0; e < E; ++e) F[e] = p.rope_turns[c * E + e];
   const int nw = gridDim.x * (blockDim.x >> 5);
+  wait_then_let_start();
   for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < p.n_rows; r += nw) {
     const int64_t slot = p.slot_map[r];
     if (slot < 0) continue;  // a padding row
@@ -316,33 +318,23 @@ cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st) 
   cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(pgd::page_plan_kernel),
                                   sizeof(int32_t) * (5 * (size_t)kPagedMaxReq + 3), ready);
   if (e != cudaSuccess) return e;
-  pgd::page_plan_kernel<<<1, pgd::kPlanThreads, smem, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(pgd::page_plan_kernel, dim3(1), dim3(pgd::kPlanThreads), smem, st, p);
   if (e != cudaSuccess || p.sums == nullptr) return e;
-  cudaLaunchConfig_t cfg{};
   const int per = 4 * pgd::kFillThreads;
-  cfg.gridDim = dim3((unsigned)std::min(((int64_t)p.max_rows + per - 1) / per, (int64_t)sms * 8));
-  cfg.blockDim = dim3(pgd::kFillThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pgd::page_fill_kernel, p);
+  const int grid = (int)std::min(((int64_t)p.max_rows + per - 1) / per, (int64_t)sms * 8);
+  return launch_early(pgd::page_fill_kernel, dim3(grid), dim3(pgd::kFillThreads), 0, st, p);
 }
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
                                 cudaStream_t st) {
   if (p.n_rows == 0) return cudaSuccess;
   const int grid = std::min((p.n_rows + 3) / 4, sms * 8);
+  auto go = [&](auto kernel) { return launch_early(kernel, dim3(grid), dim3(128), 0, st, p); };
   if (dtype == 1)
-    d == 128 ? pgd::paged_append_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(p)
-             : pgd::paged_append_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(p);
-  else
-    d == 128 ? pgd::paged_append_kernel<float, 128><<<grid, 128, 0, st>>>(p)
-             : pgd::paged_append_kernel<float, 64><<<grid, 128, 0, st>>>(p);
-  return cudaGetLastError();
+    return d == 128 ? go(pgd::paged_append_kernel<__nv_bfloat16, 128>)
+                    : go(pgd::paged_append_kernel<__nv_bfloat16, 64>);
+  return d == 128 ? go(pgd::paged_append_kernel<float, 128>)
+                  : go(pgd::paged_append_kernel<float, 64>);
 }
 
 }  // namespace msa

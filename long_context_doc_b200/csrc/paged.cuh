@@ -8,6 +8,12 @@
 
 namespace msa {
 
+// The kernels before this one in the stream are complete; the next one may be set up.
+__device__ __forceinline__ void wait_then_let_start() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 struct PagedReq {
   int a, T, L, C;  // first row, new tokens, local rows, memory rows
 };

@@ -231,8 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   const int Gq = p.h_q / p.h_kv;
   if (tid < D / 2) turns[tid] = p.rope_turns[tid];
 
-  // the dependent merge kernel may be set up while this one runs (it waits for the results)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_then_let_start();  // the tcgen05 kernel or the merge, which wait for the results
   if (tid == 0) cta_err = 0;
   __syncthreads();
   int err = 0;
@@ -801,7 +800,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) paged_merge_kernel(PagedAtte
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Gq = p.h_q / p.h_kv, TB = 256 / Gq;
   if (tid == 0) code = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_then_let_start();
   if (blockIdx.x == 0)  // the call's status word
     for (int i = tid; i < n_cta; i += kMergeThreads)
       if (p.err_cta[i]) code = p.err_cta[i];
@@ -987,25 +986,15 @@ cudaError_t launch(const PagedAttendParams& p, const PagedPlan& pl, cudaStream_t
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(kfn), kMaxSmem, ready);
   if (e != cudaSuccess) return e;
-  kfn<<<pl.grid, kThreads, pl.smem, st>>>(p, pl.S);
-  e = cudaGetLastError();
+  e = launch_early(kfn, dim3(pl.grid), dim3(kThreads), pl.smem, st, p, pl.S);
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2) {  // its CTAs start as the warp-level kernel's end
     if (pl.tc_grid > 0) e = launch_paged_attend_tc(p, pl.tc_grid, D, st);
     if (e != cudaSuccess) return e;
   }
   // the merge kernel is launched while the attention runs and waits for it on the device
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pl.grid * 3);  // one wave
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, p, pl.S, pl.tc_grid,
-                            pl.grid + pl.tc_grid);
+  return launch_early(paged_merge_kernel<T, D>, dim3(pl.grid * 3), dim3(kMergeThreads), 0, st, p,
+                      pl.S, pl.tc_grid, pl.grid + pl.tc_grid);  // one wave
 }
 
 }  // namespace pga

@@ -927,17 +927,7 @@ cudaError_t launch(const PagedAttendParams& p, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> ready{0};
   cudaError_t e = allow_smem_once(reinterpret_cast<const void*>(kfn), Cfg<D>::smem, ready);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<D>::smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kfn, mk, mv, mck, mcv, p);
+  return launch_early(kfn, dim3(grid), dim3(kThreads), Cfg<D>::smem, st, mk, mv, mck, mcv, p);
 }
 
 }  // namespace pgt
