@@ -31,6 +31,7 @@ namespace pgd {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanOneCta = 4096;  // rows up to which a single CTA fills the maps
 constexpr int kFillThreads = 256;
+constexpr int kAppendCtas = 8;     // CTAs of the append that an SM holds: its grid is one wave
 
 // what the sums leave for the fill
 struct PlanHead {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kFillThreads) page_fill_kernel(PagePlanParams 
 // i, i + d/2), so a row's angles are computed once and serve every head. HBM-bound for many
 // rows (each row read and written once), latency for few.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendParams p) {
+__global__ void __launch_bounds__(128, kAppendCtas) paged_append_kernel(PagedAppendParams p) {
   constexpr int E = 16 / sizeof(T);   // elements of a chunk
   constexpr int HC = D / 2 / E;       // chunks of half a head
   constexpr int HPW = 32 / HC;        // heads a warp takes at once
@@ -328,7 +329,7 @@ cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st) 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
                                 cudaStream_t st) {
   if (p.n_rows == 0) return cudaSuccess;
-  const int grid = std::min((p.n_rows + 3) / 4, sms * 8);
+  const int grid = std::min((p.n_rows + 3) / 4, sms * pgd::kAppendCtas);
   auto go = [&](auto kernel) { return launch_early(kernel, dim3(grid), dim3(128), 0, st, p); };
   if (dtype == 1)
     return d == 128 ? go(pgd::paged_append_kernel<__nv_bfloat16, 128>)
