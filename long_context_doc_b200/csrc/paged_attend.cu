@@ -7,11 +7,10 @@
 // attends over the request's memory rows and its local rows <= j (keys stored rotated):
 //   O = softmax(scale q . k) v, 0 where nothing is visible.
 //
-// The kernel of this file streams each key row once per 16 query rows (bf16: 8) and is the one for few
-// query rows per KV head (single tokens) and for fp32. A warp works alone: for one KV head it
-// takes a contiguous range of the flattened list (request, block of query rows, tile of
-// keys), copies the tiles with cp.async into its own ring in shared memory (no barrier between
-// warps), forms the scores and P V with warp-level MMAs (bf16; fp32 as three tf32 products of
+// The kernel of this file streams each key row once per 16 query rows (bf16: 8) and is the one for
+// few query rows per KV head (single tokens) and for fp32. A warp works alone: for one KV head it
+// takes a contiguous range of the flattened list (request, block of query rows, tile of keys),
+// copies the tiles with cp.async into its own ring in shared memory (no barrier between warps), forms the scores and P V with warp-level MMAs (bf16; fp32 as three tf32 products of
 // the operands' high and low parts) and keeps the running maximum and sum of the softmax in
 // registers. All ranges of a head have the same number of tiles to within one, whatever the
 // requests' lengths; consecutive warps take the KV heads of the same range, so their copies

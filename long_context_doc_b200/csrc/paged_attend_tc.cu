@@ -7,16 +7,23 @@
 // partial for the merge kernel. A block is two halves of 128 rows (TMEM lanes), each with its
 // own scores and accumulator in TMEM, worked on in alternation: while one half's softmax runs,
 // the tensor cores form the other half's products, and both halves use every K and V tile that
-// was loaded. Warp 0 copies the tiles (one TMA box of 64 dims per page and half a head) into a
-// ring of K and V tiles, and a block's queries, which the warp-level kernel has rotated, rounded to
-// bf16 and laid out as the operand wants them; one thread of warp 1 issues tcgen05.mma: S = Q K^T, then O += P V with P
-// read from TMEM, where the softmax put it over the scores, and V as an MN-major operand as
-// stored. Warps 2-9 hold one query row per thread: they load the 128 scores of a tile from TMEM once, mask, and keep the running maximum (raised, with
-// O rescaled in TMEM, only when a tile's maximum passes it by more than 8 in log2 units) and sum
-// in fp32. With two halves a half's completed scores imply its earlier products (the issuing
-// thread's MMAs complete in order), so O is rescaled without further waits. A
-// block of one half has both scores buffers to itself: the scores of a tile are formed before
-// the product of the tile before it.
+// was loaded. Warp 0 walks the share, announces its blocks to the others and copies the tiles (one
+// TMA box of 64 dims per page and half a head) into a ring, and a block's queries, which the
+// warp-level kernel has rotated, rounded to bf16 and laid out as the operand wants them. Warp 1
+// issues tcgen05.mma: S = Q K^T, then O += P V with P read from TMEM, where the softmax put it
+// over the scores, and V as an MN-major operand as stored. Warps 2-9 hold one query row per
+// thread: they load the 128 scores of a tile from TMEM once, mask, and keep the running maximum
+// (raised, with O rescaled in TMEM, only when a tile's maximum passes it by more than 8 in log2
+// units) and sum in fp32, and hand over the probabilities half a tile at a time. With two halves a
+// half's completed scores imply its earlier products (the issuing thread's MMAs complete in
+// order), so O is rescaled without further waits. A block of one half has both scores buffers to
+// itself: the scores of a tile are formed before the product of the tile before it, and with the
+// queries' low parts too (their place in shared memory is the other half's).
+// Roundings: the probabilities to bf16 once, the queries of two halves as well (the mean error is
+// 1.7 times that of the output's own rounding; one half: 1.4 times). The probabilities' low parts
+// would add 27% to a long chunk's time, the queries' need 64 KB that two halves do not have.
+// Bound by the chain scores -> softmax -> product: tensor pipe and exponentials are each busy half
+// of the time (2,048 tokens over 32,768 rows: 0.98 ms, 1.09 PFLOP/s).
 // Every wait is bounded; on expiry the CTA records kErrWaitTimeout, lets its copies and MMAs
 // land, frees its TMEM and leaves the rest unwritten.
 #include <cuda.h>
@@ -174,8 +181,12 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t par, int* 
 }
 
 // ------------------------------------------------------------------ the list of work
-// Geometry shared by all roles: blocks of TB = 256 / Gq tokens (rows t * Gq + head of the
-// group); a block's tiles are the memory's and the local ones up to its last token's row.
+// Blocks of TB = 256 / Gq tokens (rows t * Gq + head of the group); a block's tiles are the memory's
+// and the local ones up to its last token's row. The list counts a unit for each tile (of one half
+// or two: both take as long as their chain of products and softmax) and kStart before a block's
+// first one. A tile belongs to the share that holds its unit. (24 mixed requests: 356 us with
+// kStart = 0, 345 with 1, 342 with 2 and 3, 346 with 4; half a unit for a tile of one half: 365.)
+constexpr int kStart = 2;
 struct Work {
   PagedReq q;
   int r, head, blk, nb, CT;
@@ -184,21 +195,18 @@ struct Work {
   int toks, rows;    // tokens and query rows of the block
   int first;         // local row of its first token
   int more;          // the share goes on after it
-};
-struct Share {
-  int64_t x1, total;  // end of this CTA's share, tiles of the list
-  int G;              // shares
+  int last_share;    // the share that ends a block which this one begins and does not end
 };
 struct Walk {
   const PagedAttendParams& p;
   int Gq, TB;
-  int left;          // tiles of the share still to hand out
+  int64_t start, x1;  // first unit of the current block, end of the share
   __device__ __forceinline__ int blocks(const PagedReq& q) const { return (q.T + TB - 1) / TB; }
   __device__ __forceinline__ int tiles(const PagedReq& q, int blk) const {
     const int last = q.L - q.T + min(q.T, (blk + 1) * TB);  // rows the last token sees
     return max(1, (q.C + kN - 1) / kN + (max(last, 0) + kN - 1) / kN);
   }
-  // Tiles of the request's first n blocks of one KV head. Of full blocks it is
+  // Units of the request's first n blocks of one KV head. The tiles of full blocks are
   // n CT + sum_{b < n} floor((x + TB b) / 128) with x = L - T + TB + 127, a sum of floors
   // that needs no loop where TB divides 128 or is a multiple of it.
   __device__ __forceinline__ int64_t first_blocks(const PagedReq& q, int n) const {
@@ -220,20 +228,21 @@ struct Walk {
       }
     }
     for (; b < n; ++b) sum += tiles(q, b);
-    return sum;
+    return sum + (int64_t)n * kStart;
   }
-  __device__ __forceinline__ int64_t request_tiles(const PagedReq& q) const {
+  __device__ __forceinline__ int64_t request_units(const PagedReq& q) const {
     return first_blocks(q, blocks(q));
   }
-  __device__ __forceinline__ void set(Work& w, int from) {
+  // The current block's tiles from unit `from` on, up to the share's end.
+  __device__ __forceinline__ void set(Work& w, int64_t from) {
     w.n_tiles = tiles(w.q, w.blk);
     w.toks = min(TB, w.q.T - w.blk * TB);
     w.rows = w.toks * Gq;
     w.first = w.q.L - w.q.T + w.blk * TB;
-    w.t0 = from;
-    w.t1 = min(w.n_tiles, from + left);
-    left -= w.t1 - from;
-    w.more = left > 0;
+    const int64_t tile0 = start + kStart, n = w.n_tiles;
+    w.t0 = (int)min(max(from - tile0, (int64_t)0), n);
+    w.t1 = (int)min(max(x1 - tile0, (int64_t)0), n);
+    w.more = x1 > tile0 + n + kStart;  // the next block's first tile
   }
   __device__ __forceinline__ void enter(Work& w, int r) {
     int ignore = 0;
@@ -242,10 +251,11 @@ struct Walk {
     w.nb = blocks(w.q);
     w.CT = (w.q.C + kN - 1) / kN;
   }
-  // The first block of a share that starts `off` tiles into request r's.
-  __device__ __forceinline__ void first(Work& w, int r, int64_t off) {
+  // The block that holds the share's first unit x0, `off` units into request r's. It may have no
+  // tile left for the share.
+  __device__ __forceinline__ void first_of(Work& w, int r, int64_t off, int64_t x0) {
     enter(w, r);
-    const int64_t per_head = request_tiles(w.q);
+    const int64_t per_head = request_units(w.q);
     const bool small = ((off | per_head) >> 32) == 0;  // a 64-bit division is ten times a 32-bit one
     w.head = small ? (int)((uint32_t)off / (uint32_t)per_head) : (int)(off / per_head);
     const int64_t rem = off - w.head * per_head;
@@ -257,10 +267,12 @@ struct Walk {
       else hi = mid;
     }
     w.blk = lo;
-    set(w, (int)(rem - first_blocks(w.q, lo)));
+    start = x0 - rem + first_blocks(w.q, lo);
+    set(w, x0);
   }
-  // The next block (whole warps; called only while left > 0, so there is one).
+  // The next block (whole warps; called only where w.more says that there is one).
   __device__ __forceinline__ void next(Work& w, int lane) {
+    start += kStart + w.n_tiles;
     if (++w.blk == w.nb) {
       w.blk = 0;
       if (++w.head == p.h_kv) {
@@ -278,7 +290,7 @@ struct Walk {
         }
       }
     }
-    set(w, 0);
+    set(w, start);
   }
 };
 
@@ -317,7 +329,6 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   __shared__ int abort_word;
   __shared__ uint32_t tmem_holder;
   __shared__ Work blocks[kQueue];
-  __shared__ Share share;
   __shared__ int4 tail_item;
   __shared__ int tail_head;
   volatile int* abort_flag = &abort_word;
@@ -357,10 +368,10 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   __syncthreads();
 
   // the CTA's share of the list: total tiles first, then the request that holds the share's start
-  Walk walk{p, Gq, 2 * kHalf / Gq, 0};
+  Walk walk{p, Gq, 2 * kHalf / Gq, 0, 0};
   int err = 0;
   int64_t total = 0, mine = 0;
-  int G = 1;  // shares: no more than tiles, so that none of them is empty
+  int G = 1;  // shares: no more than units, so that none inside a block is without a tile
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     const int64_t x0 = pass ? total * blockIdx.x / G : 0;
@@ -371,7 +382,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       if (pass == 0 || p.n_req > kThreads) {
         v = 0;
         if (r < p.n_req)
-          v = walk.request_tiles(paged_req(p, r, p.tc_rows, INT_MAX, &err)) * p.h_kv;
+          v = walk.request_units(paged_req(p, r, p.tc_rows, INT_MAX, &err)) * p.h_kv;
         mine = v;
       }
       int64_t inc = v;
@@ -401,9 +412,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
   }
   const bool work = (int)blockIdx.x < G;   // then start_r is set
   const int64_t x0 = work ? total * blockIdx.x / G : 0;
-  const int64_t x1 = work ? total * (blockIdx.x + 1) / G : 0;
-  walk.left = (int)(x1 - x0);
-  if (tid == 0) share = Share{x1, total, G};
+  walk.x1 = work ? total * (blockIdx.x + 1) / G : 0;
 
   if (work) {
     if (warp == 0) {  // scores of the halves at columns 0 and 128, accumulators at 256 and 384
@@ -423,7 +432,8 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       // ---------------- walks the share, announces its blocks and copies their queries and tiles,
       // one page (or memory tile) and 64 dims a lane
       Work w;
-      walk.first(w, start_r, start_off);
+      walk.first_of(w, start_r, start_off, x0);
+      if (w.t0 == w.t1 && w.more) walk.next(w, lane);
       uint32_t seq = 0;
       const int ps = 1 << p.page_shift;
       const int br = min(ps, kN);               // rows of a box
@@ -457,6 +467,10 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       // the rotated queries are written by the grid launched before this one
       asm volatile("griddepcontrol.wait;" ::: "memory");
       while (ok) {
+        if (w.t0 == 0 && w.t1 < w.n_tiles) {  // goes on in the next shares: that of its last tile
+          const int64_t end = walk.start + kStart + w.n_tiles;
+          w.last_share = (int)((end * G + total - 1) / total - 1);
+        }
         if (lane == 0) {
           const int b = nb % kQueue;
           ok = nb < kQueue || wait_or_abort(&bempty[b], (nb / kQueue - 1) & 1, &cta_err, abort_flag);
@@ -467,7 +481,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         }
         ++nb;
         ok = uniform(ok) != 0;
-        if (!ok) break;
+        if (!ok || w.t0 == w.t1) break;  // (a share without a tile: the others see as much)
         // the block's queries, once the scores of the block before are formed: a half's rows are
         // consecutive in each slice of its head's; one half's low parts take the other's place
         const bool two = w.rows > kHalf;
@@ -590,6 +604,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         const int n = uniform(blocks[bq].t1 - blocks[bq].t0);
         const bool two = uniform(blocks[bq].rows) > kHalf, more = uniform(blocks[bq].more) != 0;
         if (lane == 0) mbar_arrive(&bempty[bq]);
+        if (n == 0) break;
         if (two) {
           // two halves in alternation, each with its own scores
           ok = wait_ring(seq);
@@ -687,6 +702,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
         const Work& w = blocks[nb % kQueue];
         const bool two = w.rows > kHalf;
         const bool active = h == 0 || two;
+        if (w.t0 == w.t1) break;
         const int t0 = w.t0, t1 = w.t1, CT = w.CT, n_ctx = w.q.C, n_loc = w.q.L;
         const bool more = w.more != 0;
         const bool any_row = h * kHalf + (warp & 3) * 32 < w.rows;  // of the warp
@@ -870,9 +886,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
           fence_before();  // O is read before the next block's products
         }
         if (begins && !ends && tid == 64) {  // goes on in the next CTAs' shares
-          const int64_t end = share.x1 - t1 + w.n_tiles;
-          tail_item = make_int4(w.q.a, w.q.T, w.blk,
-                                (int)((end * share.G + share.total - 1) / share.total - 1));
+          tail_item = make_int4(w.q.a, w.q.T, w.blk, w.last_share);
           tail_head = w.head;
         }
         __syncwarp();
