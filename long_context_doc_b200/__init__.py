@@ -12,6 +12,7 @@ The lower-case helpers (``encode_pool``, ``route_topk``, ``gather``, ``sparse_at
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -646,7 +647,9 @@ def aux_routing_loss(Q_r, Kbar_r, positive_bits, tau: float = 0.1, stream=None):
 
 # ----------------------------------------------------------------------------- paged context
 # These calls are made per layer and token, so their argument checks are one expression on the
-# way in; what it finds wrong is named by the _explain_* functions afterwards.
+# way in; what it finds wrong is named by the _explain_* functions afterwards. With ``stream`` a
+# call runs there, and the outputs and workspaces that it was not given are made there too, as
+# under torch.cuda.stream(stream).
 def _need(what: str, ok: bool, text: str):
     if not ok:
         raise MSAError(1, f"{what}: {text}")
@@ -679,15 +682,32 @@ def _explain_pool(what: str, K_pages, V_pages):
                     V_pages=(V_pages, K_pages.dtype, None))
 
 
+def _raw_stream(dev: int, stream) -> int:
+    """Handle of ``stream``, or of the current one of device ``dev``."""
+    if stream is None:
+        # the raw handle of torch.cuda.current_stream(dev), at a twentieth of its 3 us
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _made_on(dev: int, stream):
+    """Context in which a call makes the tensors that it was not given: its own stream's. What
+    fills them comes before the call's kernels there, and their memory is not handed on to other
+    work of the current stream while these run."""
+    if stream is None or dev < 0:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _raw_stream(dev, stream)
+        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle else
+                  torch.cuda.default_stream(dev))
+    return torch.cuda.stream(stream)
+
+
 def _launch(dev: int, stream, f, *args):
     """f(*args, stream) with device ``dev`` current, on ``stream`` or the device's current one."""
     if dev < 0:
         raise MSAError(1, "the tensors are not in device memory")
-    if stream is None:
-        # the raw handle of torch.cuda.current_stream(dev), at a twentieth of its 3 us
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
+    stream = _raw_stream(dev, stream)
     if torch.cuda.current_device() == dev:
         status = f(*args, stream)
     else:
@@ -711,12 +731,12 @@ def page_plan(target, length, n_free, block_table, free_list, page_size: int, ma
     [n_req, max_pages] and ``free_list`` [n_pages] are updated in place; returns dict(length,
     n_free, row_start, slot_map, row_pos). ``out`` gives these tensors (its length and n_free
     may be the arguments themselves); device-side errors are in the status word of ``ws``."""
-    n_req = block_table.shape[0]
-    if out is None:
-        out = page_plan_buffers(n_req, max_rows, block_table.device)
-    if ws is None:
-        ws = _ws(msa_page_plan_workspace(n_req, max_rows), block_table.device)
-    dev = block_table.get_device()
+    n_req, dev = block_table.shape[0], block_table.get_device()
+    with _made_on(dev, stream):
+        if out is None:
+            out = page_plan_buffers(n_req, max_rows, block_table.device)
+        if ws is None:
+            ws = _ws(msa_page_plan_workspace(n_req, max_rows), block_table.device)
     wanted = ((target, n_req), (length, n_req), (n_free, 1), (free_list, free_list.numel()),
               (block_table, block_table.numel()), (out["length"], n_req), (out["n_free"], 1),
               (out["row_start"], n_req + 1), (out["slot_map"], max_rows),
@@ -743,9 +763,10 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
     """Writes a step's new rows [n_rows, h_kv, d] (rows of any stride) into their pages, keys
     rotated at pos0 + row_pos. Returns the workspace, whose status word a bad slot sets; pass
     the plan's as ``ws`` to read one status a step."""
-    if ws is None:
-        ws = torch.zeros(256, dtype=torch.uint8, device=K_pages.device)
     dt, dev, i32 = K_pages.dtype, K_pages.get_device(), torch.int32
+    if ws is None:
+        with _made_on(dev, stream):
+            ws = torch.zeros(256, dtype=torch.uint8, device=K_pages.device)
     n_rows, h_kv, d = K_new.shape
     if not (K_pages.dim() == 4 and K_pages.shape == V_pages.shape and
             K_pages.shape[2:] == K_new.shape[1:] and K_new.shape == V_new.shape and
@@ -787,7 +808,8 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
     n_req, max_pages = block_table.shape
     max_ctx = 0 if ctxK is None else ctxK.shape[1]
     if O is None:
-        O = torch.empty((n_rows, h_q, d), dtype=dt, device=K_pages.device)
+        with _made_on(dev, stream):
+            O = torch.empty((n_rows, h_q, d), dtype=dt, device=K_pages.device)
     if not (K_pages.shape == V_pages.shape and K_pages.shape[3] == d and O.shape == Q.shape and
             V_pages.dtype == dt and Q.dtype == dt and O.dtype == dt and
             row_start.dtype == i32 and length.dtype == i32 and block_table.dtype == i32 and
@@ -818,8 +840,9 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
                         ctxK=(ctxK, dt, None), ctxV=(ctxV, dt, None),
                         ctx_len=(ctx_len, i32, n_req))
     if ws is None:
-        ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q), max_ctx,
-                                            max_pages, page), Q.device)
+        with _made_on(dev, stream):
+            ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q),
+                                                max_ctx, max_pages, page), Q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         _explain_arrays("paged_attend", dev, ws=(ws, None, None))
     if ctxK is None:
@@ -841,7 +864,9 @@ class PagedCache:
     block table, one stack of free pages and one array of lengths for all layers, in device
     memory. A step is ``plan`` once, then ``append`` and ``attend`` of each layer; the calls
     read the lengths on the device, so a captured step replays as the requests grow, end
-    (target 0) and begin. Keys are stored rotated at pos0 + row (RoPE base ``rope_base``)."""
+    (target 0) and begin. Keys are stored rotated at pos0 + row (RoPE base ``rope_base``). The
+    tensors of the cache are made on the current stream; who uses it on another orders the two
+    and keeps the cache until that work is done."""
 
     def __init__(self, n_req: int, n_pages: int, page_size: int, max_pages: int, max_rows: int,
                  h_kv: int, d: int, n_layers: int = 1, pos0: int = 0, rope_base: float = 0.0,
@@ -858,7 +883,9 @@ class PagedCache:
         self.length, self.n_free = self.out["length"], self.out["n_free"]
         self.ws = torch.zeros(max(256, msa_page_plan_workspace(n_req, max_rows)),
                               dtype=torch.uint8, device=device)
-        self._attend_ws = []  # all kept: a captured step goes on using the one it was given
+        # stream -> workspaces made there, all kept: a captured step goes on using the one it was
+        # given
+        self._attend_ws = {}
 
     def plan(self, target, stream=None) -> dict:
         """Moves every request to its target length (int32 [n_req], device memory) and returns
@@ -874,16 +901,20 @@ class PagedCache:
     def attend(self, layer: int, Q, ctxK=None, ctxV=None, ctx_len=None, scale: float = 0.0, O=None,
                ws=None, stream=None):
         """Attention of the planned rows' queries Q [rows, h_q, d] of a layer. Without ``ws`` the
-        cache's own workspace serves: calls that overlap on the GPU need one each."""
+        cache's own workspace of the stream serves: calls that overlap on the GPU all the same
+        (replays of two captured steps) need one each."""
         if ws is None:
             n_req, max_pages = self.block_table.shape
+            dev = self.K.get_device()
+            kept = self._attend_ws.setdefault(_raw_stream(dev, stream), [])
             need = msa_paged_attend_workspace(Q.shape[0], n_req, Q.shape[1], self.K.shape[3],
                                               self.K.shape[4], dtype_code(self.K),
                                               0 if ctxK is None else ctxK.shape[1], max_pages,
                                               self.page_size)
-            if not self._attend_ws or self._attend_ws[-1].numel() < need:
-                self._attend_ws.append(_ws(need, self.K.device))
-            ws = self._attend_ws[-1]
+            if not kept or kept[-1].numel() < need:
+                with _made_on(dev, stream):
+                    kept.append(_ws(need, self.K.device))
+            ws = kept[-1]
         return paged_attend(Q, self.out["row_start"], self.length, self.K[layer], self.V[layer],
                             self.block_table, self.pos0, self.rope_base, ctxK, ctxV, ctx_len,
                             scale, O, ws, stream)

@@ -1,0 +1,91 @@
+"""What the paged local context promises beside its numbers: streams, errors, limits."""
+import numpy as np
+import pytest
+import torch
+
+from test_paged import BASE, Case, _i32, _plan_state, gpu_test, msa, plan64  # noqa: F401
+
+SLEEP = 60_000_000  # SM clocks, some 30 ms
+
+
+# ------------------------------------------------------------------ streams
+@gpu_test
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_plan_on_another_stream(msa, gpu, raw):
+    """The outputs that page_plan makes are filled on its stream, before its kernel, however
+    late the current stream runs."""
+    lens, target = [37, 0, 16], [38, 5, 16]
+    table, free, n_free = _plan_state(np.random.RandomState(1), lens, 16, 5, 20)
+    ref, _, _ = plan64(target, lens, table, free, n_free, 16, 12)
+    t, f = torch.from_numpy(table).to(gpu), torch.from_numpy(free).to(gpu)
+    args = _i32(target, gpu), _i32(lens, gpu), _i32([n_free], gpu)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SLEEP)  # the current stream
+    out = msa.page_plan(*args, t, f, 16, 12, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert {k: v.cpu().tolist() for k, v in out.items()} == ref
+
+
+@gpu_test
+def test_append_status_on_another_stream(msa, gpu):
+    K = torch.zeros(2, 16, 2, 64, device=gpu)
+    V, new = torch.zeros_like(K), torch.ones(1, 2, 64, device=gpu)
+    slot, pos = _i32([32], gpu), _i32([0], gpu)  # past the pool
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SLEEP)
+    ws = msa.paged_append(K, V, slot, pos, new, new, 0, 0.0, stream=side)
+    torch.cuda.synchronize()
+    assert msa.msa_workspace_status(ws, side) == 3
+
+
+@gpu_test
+@pytest.mark.parametrize("cached", [False, True], ids=["helper", "cache"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attend_on_another_stream(msa, gpu, dtype, cached):
+    """The workspace that paged_attend makes is not handed to the current stream while the
+    call's kernels have yet to run."""
+    c = Case(gpu, 71, dtype, [2000, 300], [1, 40], 32, 16, 4, 128, [64, 2])
+    size = c.workspace(msa).numel()
+    side = torch.cuda.Stream()
+    cache = None
+    if cached:
+        cache = msa.PagedCache(2, c.K.shape[0], 32, c.table.shape[1], c.total, 4, 128,
+                               pos0=c.pos0, rope_base=c.base, dtype=c.tt, device=gpu)
+        cache.K[0].copy_(c.K)
+        cache.V[0].copy_(c.V)
+        cache.block_table.copy_(c.table)
+        cache.length.copy_(c.length)
+        cache.out["row_start"].copy_(c.row_start)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SLEEP)
+    if cached:
+        O = cache.attend(0, c.Q, **c.ctx, stream=side)
+    else:
+        O = c.run(msa, stream=side)
+    junk = [torch.full((size,), 0x7F, dtype=torch.uint8, device=gpu) for _ in range(4)]
+    junk += [torch.full(tuple(O.shape), 9.0, dtype=O.dtype, device=gpu) for _ in range(4)]
+    torch.cuda.synchronize()
+    c.check(O)
+    assert all(bool((j == (0x7F if j.dtype == torch.uint8 else 9.0)).all()) for j in junk)
+
+
+@gpu_test
+def test_cache_has_a_workspace_a_stream(msa, gpu):
+    """Calls of one cache on two streams may overlap."""
+    cache = msa.PagedCache(2, 200, 16, 100, 400, 2, 128, rope_base=BASE, device=gpu)
+    f = lambda *s: torch.randn(*s, device=gpu).bfloat16()
+    cache.plan(_i32([300, 100], gpu))
+    cache.append(0, f(400, 2, 128), f(400, 2, 128))
+    q = [f(400, 8, 128), f(400, 8, 128)]
+    want = [cache.attend(0, x)[:400].clone() for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            got[i].append(cache.attend(0, q[i], stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for g, w in zip(got, want) for x in g)
