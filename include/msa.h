@@ -548,6 +548,10 @@ msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32
  * is computed).
  * ws         msa_paged_attend_workspace(...) bytes, 256-byte aligned, not shared with a call
  *            that runs at the same time. The result does not depend on its contents.
+ * msa_paged_attend_step is the same call as a part of a step: a status that is not 0 is recorded
+ * in the status word of step_ws too, which the call only ever sets, as msa_paged_append does.
+ * Given the plan's workspace, one status word tells of a step's plan, appends and attentions.
+ * step_ws NULL: msa_paged_attend.
  */
 size_t msa_paged_attend_workspace(int32_t n_rows, int32_t n_req, int32_t h_q, int32_t h_kv,
                                   int32_t d, int32_t dtype, int32_t max_ctx, int32_t max_pages,
@@ -560,6 +564,14 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
                             int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
                             int32_t pos0, float rope_base, float scale, void* O, void* ws,
                             size_t ws_bytes, void* stream);
+msa_status msa_paged_attend_step(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
+                                 const int32_t* row_start, const int32_t* len, int32_t n_req,
+                                 const void* K_pages, const void* V_pages, int32_t n_pages,
+                                 int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                 const void* ctxK, const void* ctxV, const int32_t* ctx_len,
+                                 int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
+                                 int32_t pos0, float rope_base, float scale, void* O, void* ws,
+                                 size_t ws_bytes, void* step_ws, void* stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,7 @@ SYMBOLS = ("msa_status_string", "msa_last_error", "msa_version", "msa_set_device
            "msa_encode_hidden", "msa_sparse_attend_backward_workspace",
            "msa_sparse_attend_backward", "msa_scatter_bank_grad", "msa_aux_routing_loss_workspace",
            "msa_aux_routing_loss", "msa_page_plan_workspace", "msa_page_plan", "msa_paged_append",
-           "msa_paged_attend_workspace", "msa_paged_attend")
+           "msa_paged_attend_workspace", "msa_paged_attend", "msa_paged_attend_step")
 
 
 class MSAError(RuntimeError):
@@ -143,6 +143,8 @@ def _load():
     L.msa_paged_attend.restype = ctypes.c_int
     L.msa_paged_attend.argtypes = [vp, i64, i32, i32, vp, vp, i32, vp, vp, i32, i32, vp, i32, vp,
                                    vp, vp, i32, i32, i32, i32, i32, f32, f32, vp, vp, sz, vp]
+    L.msa_paged_attend_step.restype = ctypes.c_int
+    L.msa_paged_attend_step.argtypes = [*L.msa_paged_attend.argtypes, vp]
     return L
 
 
@@ -428,15 +430,22 @@ def msa_paged_attend(Q, row_start, length, K_pages, V_pages, block_table, ctxK, 
                      pos0, rope_base, scale, O, ws, stream=None):
     """Q [n_rows, h_q, d], rows of any stride; O [n_rows, h_q, d]; ctxK, ctxV, ctx_len may be
     None (no routed memory)."""
+    msa_paged_attend_step(Q, row_start, length, K_pages, V_pages, block_table, ctxK, ctxV, ctx_len,
+                          pos0, rope_base, scale, O, ws, None, stream)
+
+
+def msa_paged_attend_step(Q, row_start, length, K_pages, V_pages, block_table, ctxK, ctxV, ctx_len,
+                          pos0, rope_base, scale, O, ws, step_ws, stream=None):
+    """msa_paged_attend, device errors recorded in the status word of ``step_ws`` too."""
     n_rows, h_q, d = Q.shape
     n_pages, page, h_kv, _ = K_pages.shape
     n_req, max_pages = block_table.shape
-    _check(lib.msa_paged_attend(_p(Q), Q.stride(0), n_rows, h_q, _p(row_start), _p(length), n_req,
-                                _p(K_pages), _p(V_pages), n_pages, page, _p(block_table),
-                                max_pages, _p(ctxK), _p(ctxV), _p(ctx_len),
-                                0 if ctxK is None else ctxK.shape[1], h_kv, d, dtype_code(Q),
-                                pos0, rope_base, scale, _p(O), _p(ws),
-                                ws.numel() * ws.element_size(), _s(stream)))
+    _check(lib.msa_paged_attend_step(_p(Q), Q.stride(0), n_rows, h_q, _p(row_start), _p(length),
+                                     n_req, _p(K_pages), _p(V_pages), n_pages, page,
+                                     _p(block_table), max_pages, _p(ctxK), _p(ctxV), _p(ctx_len),
+                                     0 if ctxK is None else ctxK.shape[1], h_kv, d, dtype_code(Q),
+                                     pos0, rope_base, scale, _p(O), _p(ws),
+                                     ws.numel() * ws.element_size(), _p(step_ws), _s(stream)))
 
 
 # ----------------------------------------------------------------------------- helpers
@@ -798,10 +807,12 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
 
 def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
                  rope_base: float, ctxK=None, ctxV=None, ctx_len=None, scale: float = 0.0, O=None,
-                 ws=None, stream=None):
+                 ws=None, stream=None, step_ws=None):
     """Attention of every request's new tokens Q [n_rows, h_q, d] (packed by ``row_start``, rows
     of any stride) over [routed memory ; paged local context of ``length`` rows]; returns O
-    [n_rows, h_q, d] (rows behind the last request's as they were)."""
+    [n_rows, h_q, d] (rows behind the last request's as they were). A device error (its rows of O
+    may be unwritten) is in the status word of ``ws``, and is recorded in that of ``step_ws`` (the
+    plan's workspace) where one is given."""
     dt, dev, i32 = K_pages.dtype, K_pages.get_device(), torch.int32
     n_rows, h_q, d = Q.shape
     n_pages, page, h_kv, _ = K_pages.shape
@@ -845,16 +856,19 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
                                                 max_ctx, max_pages, page), Q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         _explain_arrays("paged_attend", dev, ws=(ws, None, None))
+    if step_ws is not None:
+        _need("paged_attend", step_ws.get_device() == dev and step_ws.is_contiguous() and
+              step_ws.nbytes >= 256, "step_ws is not a workspace on the tensors' device")
     if ctxK is None:
         mem = (None, None, None)
     else:
         mem = (ctxK.data_ptr(), ctxV.data_ptr(), ctx_len.data_ptr())
-    _launch(dev, stream, lib.msa_paged_attend, Q.data_ptr(),
+    _launch(dev, stream, lib.msa_paged_attend_step, Q.data_ptr(),
             Q.stride(0) if n_rows > 1 else h_q * d, n_rows, h_q,
             row_start.data_ptr(), length.data_ptr(), n_req, K_pages.data_ptr(),
             V_pages.data_ptr(), n_pages, page, block_table.data_ptr(), max_pages, *mem, max_ctx,
             h_kv, d, dtype_code(Q), pos0, rope_base, scale, O.data_ptr(), ws.data_ptr(),
-            ws.nbytes)
+            ws.nbytes, None if step_ws is None else step_ws.data_ptr())
     return O
 
 
@@ -917,9 +931,9 @@ class PagedCache:
             ws = kept[-1]
         return paged_attend(Q, self.out["row_start"], self.length, self.K[layer], self.V[layer],
                             self.block_table, self.pos0, self.rope_base, ctxK, ctxV, ctx_len,
-                            scale, O, ws, stream)
+                            scale, O, ws, stream, step_ws=self.ws)
 
     def status(self, stream=None) -> int:
-        """Status word of the last plan and the appends since (0 = no device error); synchronises
-        the stream."""
+        """Status word of the last plan and the appends and attentions since (0 = no device
+        error; otherwise their outputs are not to be used); synchronises the stream."""
         return msa_workspace_status(self.ws, stream)

@@ -189,14 +189,14 @@ size_t msa_paged_attend_workspace(int32_t n_rows, int32_t n_req, int32_t h_q, in
          msa::paged_attend_plan(n_rows, n_req, h_q, h_kv, d, dtype, sm_count()).bytes();
 }
 
-msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
-                            const int32_t* row_start, const int32_t* len, int32_t n_req,
-                            const void* K_pages, const void* V_pages, int32_t n_pages,
-                            int32_t page_size, const int32_t* block_table, int32_t max_pages,
-                            const void* ctxK, const void* ctxV, const int32_t* ctx_len,
-                            int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
-                            int32_t pos0, float rope_base, float scale, void* O, void* ws,
-                            size_t ws_bytes, void* stream) {
+msa_status msa_paged_attend_step(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
+                                 const int32_t* row_start, const int32_t* len, int32_t n_req,
+                                 const void* K_pages, const void* V_pages, int32_t n_pages,
+                                 int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                 const void* ctxK, const void* ctxV, const int32_t* ctx_len,
+                                 int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
+                                 int32_t pos0, float rope_base, float scale, void* O, void* ws,
+                                 size_t ws_bytes, void* step_ws, void* stream) {
   msa_status s = check_heads(h_kv, d, dtype);
   if (s == MSA_OK) s = check_pool(page_size, n_pages, max_pages, n_req);
   if (s != MSA_OK) return s;
@@ -215,6 +215,7 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
   const size_t need = kHeader + pl.bytes();
   REQUIRE(ws != nullptr && ws_bytes >= need && aligned(ws, 256), MSA_ERR_WORKSPACE,
           "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, need);
+  REQUIRE(aligned(step_ws, 256), MSA_ERR_WORKSPACE, "the step's workspace is not 256-byte aligned");
   const int64_t per16 = 16 / (int64_t)esize(dtype);
   if (any) {
     REQUIRE(Q && row_start && len && K_pages && V_pages && block_table && O, MSA_ERR_INVALID_ARG,
@@ -260,6 +261,7 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
     return at;
   };
   p.err = reinterpret_cast<int*>(take(kHeader));
+  p.step_err = static_cast<int*>(step_ws);
   p.err_cta = reinterpret_cast<int*>(take(pl.err_bytes));
   p.tail = reinterpret_cast<int4*>(take(pl.tail_bytes));
   p.part_ml = reinterpret_cast<float*>(take(pl.ml_bytes));
@@ -271,6 +273,20 @@ msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int
   p.tc_rows = pl.tc_grid > 0 ? msa::kPagedWarpRows : INT32_MAX;
   p.tc_err_at = pl.grid;
   return done(msa::launch_paged_attend(p, pl, dtype, d, st), "msa_paged_attend launch");
+}
+
+msa_status msa_paged_attend(const void* Q, int64_t q_stride, int32_t n_rows, int32_t h_q,
+                            const int32_t* row_start, const int32_t* len, int32_t n_req,
+                            const void* K_pages, const void* V_pages, int32_t n_pages,
+                            int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                            const void* ctxK, const void* ctxV, const int32_t* ctx_len,
+                            int32_t max_ctx, int32_t h_kv, int32_t d, int32_t dtype,
+                            int32_t pos0, float rope_base, float scale, void* O, void* ws,
+                            size_t ws_bytes, void* stream) {
+  return msa_paged_attend_step(Q, q_stride, n_rows, h_q, row_start, len, n_req, K_pages, V_pages,
+                               n_pages, page_size, block_table, max_pages, ctxK, ctxV, ctx_len,
+                               max_ctx, h_kv, d, dtype, pos0, rope_base, scale, O, ws, ws_bytes,
+                               nullptr, stream);
 }
 
 }  // extern "C"

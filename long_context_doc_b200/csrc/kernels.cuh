@@ -414,6 +414,7 @@ struct PagedAttendParams {
   float scale_log2;
   void* O;                  // [n_rows, h_q, d]
   int* err;                 // status word, written by the merge kernel
+  int* step_err;            // the step's status word (nullable), only ever set
   int* err_cta;             // what each CTA recorded: [grid], then [tc_grid]
   int4* tail;               // [S] the item a range begins and does not end
   float* part_ml;           // [S][2][h_kv][8 or 16][2] partials of the warp-level kernel

@@ -856,7 +856,10 @@ __global__ void __launch_bounds__(kMergeThreads, 3) paged_merge_kernel(PagedAtte
     }
     __syncthreads();
   }
-  if (blockIdx.x == 0 && tid == 0) *p.err = code;
+  if (blockIdx.x == 0 && tid == 0) {
+    *p.err = code;
+    if (code) set_err(p.step_err, code);
+  }
   // row task t of list k: where its partials and its row of O are
   struct Row {
     const float* ml;

@@ -1,4 +1,6 @@
 """What the paged local context promises beside its numbers: streams, errors, limits."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -89,3 +91,53 @@ def test_cache_has_a_workspace_a_stream(msa, gpu):
             got[i].append(cache.attend(0, q[i], stream=s))
     torch.cuda.synchronize()
     assert all(torch.equal(x, w) for g, w in zip(got, want) for x in g)
+
+
+# ------------------------------------------------------------------ errors of a step
+def _two_request_step(msa, gpu, T, dtype=torch.bfloat16):
+    cache = msa.PagedCache(2, 40, 16, 12, 2 * T, 2, 64, rope_base=BASE, dtype=dtype, device=gpu)
+    f = lambda n, h: torch.randn(n, h, 64, device=gpu).to(dtype)
+    cache.plan(_i32([T, T], gpu))
+    cache.append(0, f(2 * T, 2), f(2 * T, 2))
+    assert cache.status() == 0
+    cache.plan(_i32([2 * T, 2 * T], gpu))
+    return cache, f
+
+
+@gpu_test
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_cache_status_covers_attention(msa, gpu, T, dtype):
+    """A bad page and queries for fewer rows than planned reach status(), and stay there until
+    the next plan."""
+    cache, f = _two_request_step(msa, gpu, T, dtype)
+    cache.append(0, f(2 * T, 2), f(2 * T, 2))
+    cache.attend(0, f(2 * T, 8))
+    assert cache.status() == 0
+    page = int(cache.block_table[1, 0])
+    cache.block_table[1, 0] = 40  # past the pool
+    cache.attend(0, f(2 * T, 8))
+    cache.block_table[1, 0] = page
+    cache.attend(0, f(2 * T, 8))  # a later layer that finds nothing wrong
+    assert cache.status() == 3
+    cache.plan(cache.length + 0)
+    assert cache.status() == 0
+    cache.plan(_i32([3 * T, 3 * T], gpu))
+    cache.append(0, f(2 * T, 2), f(2 * T, 2))
+    assert cache.status() == 0
+    cache.attend(0, f(2 * T - 1, 8))  # a planned row without its query
+    assert cache.status() == 3
+
+
+def test_attend_step_refuses_a_misaligned_word(msa):
+    ws = ctypes.c_void_p(512)
+    f = ctypes.c_void_p(1024)
+    need = msa.msa_paged_attend_workspace(4, 2, 8, 2, 64, 1, 5, 4, 16)
+    call = lambda step: msa.lib.msa_paged_attend_step(
+        f, 512, 4, 8, f, f, 2, f, f, 8, 16, f, 4, f, f, f, 5, 2, 64, 1, 0, 0.0, 0.0, f, ws, need,
+        ctypes.c_void_p(step), None)
+    assert call(520) == 3
+    pool, i32 = torch.zeros(4, 16, 2, 64), lambda *s: torch.zeros(s, dtype=torch.int32)
+    with pytest.raises(msa.MSAError, match="step_ws"):
+        msa.paged_attend(torch.zeros(5, 4, 64), i32(3), i32(2), pool, pool, i32(2, 3), 0, 0.0,
+                         step_ws=torch.zeros(8, dtype=torch.uint8))
