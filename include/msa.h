@@ -464,7 +464,7 @@ msa_status msa_encode_hidden(const void* H, int64_t n_tok, int32_t D, const void
  * counterpart). Row p of request r lies in page block_table[r, p / page_size] at row
  * p % page_size ("slot" = page * page_size + p % page_size); keys are stored rotated at
  * pos0 + p. A step is msa_page_plan once, then per layer msa_paged_append of the step's new
- * rows and msa_paged_attend of their queries. New rows lie packed, request after request:
+ * rows and msa_paged_attend of their queries (or their _step forms, which check more). New rows lie packed, request after request:
  * row_start[r] .. row_start[r + 1] are request r's. All lengths, counts and tables are int32 in
  * device memory, so a captured step replays with the current ones; rows behind the last
  * request's (padding) are neither read nor written.
@@ -511,14 +511,23 @@ msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
  * (K before RoPE, like K_loc); rows with a negative slot are skipped. K_new, V_new: n_rows rows
  * of [h_kv, d], k_stride / v_stride elements apart (for slices of a fused projection; multiples
  * of 16 bytes). Slots are distinct (rows with one slot leave a mix of them there), and the pools
- * do not overlap the inputs. A slot past the pool is skipped and recorded in the status word of ws (>= 256 bytes, 256-byte aligned), which this
- * call only ever sets: give it the plan's workspace, which msa_page_plan starts every step, or
- * one that the caller zeroes. */
+ * do not overlap the inputs. A slot past the pool is skipped and recorded (3) in the status word
+ * of ws (>= 256 bytes, 256-byte aligned), which this call only ever sets: give it the plan's
+ * workspace, which msa_page_plan starts every step, or one that the caller zeroes.
+ * msa_paged_append_step is the same call for all rows of a step at once: planned points to their
+ * count in device memory (row_start + n_req). More rows than n_rows are recorded (3), for
+ * attention would read what their places held before. planned NULL: msa_paged_append. */
 msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
                             const int32_t* slot_map, const int32_t* row_pos, const void* K_new,
                             const void* V_new, int64_t k_stride, int64_t v_stride,
                             int32_t n_rows, int32_t h_kv, int32_t d, int32_t dtype, int32_t pos0,
                             float rope_base, void* ws, size_t ws_bytes, void* stream);
+msa_status msa_paged_append_step(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
+                                 const int32_t* slot_map, const int32_t* row_pos,
+                                 const void* K_new, const void* V_new, int64_t k_stride,
+                                 int64_t v_stride, int32_t n_rows, int32_t h_kv, int32_t d,
+                                 int32_t dtype, int32_t pos0, float rope_base,
+                                 const int32_t* planned, void* ws, size_t ws_bytes, void* stream);
 
 /* msa_paged_attend - msa_sparse_attend for ragged requests over the paged local context: from
  * single tokens to long chunks, in one batch.

@@ -39,6 +39,7 @@ SYMBOLS = ("msa_status_string", "msa_last_error", "msa_version", "msa_set_device
            "msa_encode_hidden", "msa_sparse_attend_backward_workspace",
            "msa_sparse_attend_backward", "msa_scatter_bank_grad", "msa_aux_routing_loss_workspace",
            "msa_aux_routing_loss", "msa_page_plan_workspace", "msa_page_plan", "msa_paged_append",
+           "msa_paged_append_step",
            "msa_paged_attend_workspace", "msa_paged_attend", "msa_paged_attend_step")
 
 
@@ -138,6 +139,9 @@ def _load():
     L.msa_paged_append.restype = ctypes.c_int
     L.msa_paged_append.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i64, i64, i32, i32, i32, i32,
                                    i32, f32, vp, sz, vp]
+    L.msa_paged_append_step.restype = ctypes.c_int
+    L.msa_paged_append_step.argtypes = [vp, vp, i32, i32, vp, vp, vp, vp, i64, i64, i32, i32, i32,
+                                        i32, i32, f32, vp, vp, sz, vp]
     L.msa_paged_attend_workspace.restype = sz
     L.msa_paged_attend_workspace.argtypes = [i32] * 9
     L.msa_paged_attend.restype = ctypes.c_int
@@ -412,12 +416,20 @@ def msa_paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, ro
                      stream=None):
     """K_pages, V_pages [n_pages, page_size, h_kv, d]; K_new, V_new [n_rows, h_kv, d], rows of
     any stride."""
+    msa_paged_append_step(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, rope_base, None,
+                          ws, stream)
+
+
+def msa_paged_append_step(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0, rope_base,
+                          planned, ws, stream=None):
+    """msa_paged_append of a step's rows at once, ``planned`` (int32, device memory, or None) of
+    them."""
     n_pages, page, h_kv, d = K_pages.shape
-    _check(lib.msa_paged_append(_p(K_pages), _p(V_pages), n_pages, page, _p(slot_map),
-                                _p(row_pos), _p(K_new), _p(V_new), K_new.stride(0),
-                                V_new.stride(0), K_new.shape[0], h_kv, d, dtype_code(K_pages),
-                                pos0, rope_base, _p(ws), ws.numel() * ws.element_size(),
-                                _s(stream)))
+    _check(lib.msa_paged_append_step(_p(K_pages), _p(V_pages), n_pages, page, _p(slot_map),
+                                     _p(row_pos), _p(K_new), _p(V_new), K_new.stride(0),
+                                     V_new.stride(0), K_new.shape[0], h_kv, d,
+                                     dtype_code(K_pages), pos0, rope_base, _p(planned), _p(ws),
+                                     ws.numel() * ws.element_size(), _s(stream)))
 
 
 def msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype, max_ctx, max_pages,
@@ -768,10 +780,11 @@ def page_plan(target, length, n_free, block_table, free_list, page_size: int, ma
 
 
 def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, rope_base: float,
-                 ws=None, stream=None):
+                 ws=None, stream=None, row_start=None):
     """Writes a step's new rows [n_rows, h_kv, d] (rows of any stride) into their pages, keys
     rotated at pos0 + row_pos. Returns the workspace, whose status word a bad slot sets; pass
-    the plan's as ``ws`` to read one status a step."""
+    the plan's as ``ws`` to read one status a step. With the plan's ``row_start`` the rows are all
+    that it has a place for: fewer set the status word too."""
     dt, dev, i32 = K_pages.dtype, K_pages.get_device(), torch.int32
     if ws is None:
         with _made_on(dev, stream):
@@ -796,12 +809,18 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
                         row_pos=(row_pos, i32, None), ws=(ws, None, None))
         rows = min(slot_map.numel(), row_pos.numel())
         _need("paged_append", rows >= n_rows, f"slot_map and row_pos cover {rows} of {n_rows} rows")
+    planned = None
+    if row_start is not None:
+        if row_start.dtype != i32 or row_start.get_device() != dev or not row_start.is_contiguous():
+            _explain_arrays("paged_append", dev, row_start=(row_start, i32, None))
+        _need("paged_append", row_start.numel() > 0, "row_start is empty")
+        planned = row_start.data_ptr() + 4 * (row_start.numel() - 1)
     n_pages, page = K_pages.shape[:2]
-    _launch(dev, stream, lib.msa_paged_append, K_pages.data_ptr(), V_pages.data_ptr(), n_pages,
+    _launch(dev, stream, lib.msa_paged_append_step, K_pages.data_ptr(), V_pages.data_ptr(), n_pages,
             page, slot_map.data_ptr(), row_pos.data_ptr(), K_new.data_ptr(), V_new.data_ptr(),
             K_new.stride(0) if n_rows > 1 else h_kv * d,
             V_new.stride(0) if n_rows > 1 else h_kv * d, n_rows, h_kv, d, dtype_code(K_pages),
-            pos0, rope_base, ws.data_ptr(), ws.nbytes)
+            pos0, rope_base, planned, ws.data_ptr(), ws.nbytes)
     return ws
 
 
@@ -910,7 +929,8 @@ class PagedCache:
     def append(self, layer: int, K_new, V_new, stream=None):
         """Writes the planned rows (K_new, V_new [rows, h_kv, d], padding allowed) of a layer."""
         paged_append(self.K[layer], self.V[layer], self.out["slot_map"], self.out["row_pos"],
-                     K_new, V_new, self.pos0, self.rope_base, ws=self.ws, stream=stream)
+                     K_new, V_new, self.pos0, self.rope_base, ws=self.ws, stream=stream,
+                     row_start=self.out["row_start"])
 
     def attend(self, layer: int, Q, ctxK=None, ctxV=None, ctx_len=None, scale: float = 0.0, O=None,
                ws=None, stream=None):

@@ -136,11 +136,12 @@ msa_status msa_page_plan(const int32_t* target_len, const int32_t* len_in,
   return done(msa::launch_page_plan(p, sm_count(), (cudaStream_t)stream), "msa_page_plan launch");
 }
 
-msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
-                            const int32_t* slot_map, const int32_t* row_pos, const void* K_new,
-                            const void* V_new, int64_t k_stride, int64_t v_stride,
-                            int32_t n_rows, int32_t h_kv, int32_t d, int32_t dtype, int32_t pos0,
-                            float rope_base, void* ws, size_t ws_bytes, void* stream) {
+msa_status msa_paged_append_step(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
+                                 const int32_t* slot_map, const int32_t* row_pos,
+                                 const void* K_new, const void* V_new, int64_t k_stride,
+                                 int64_t v_stride, int32_t n_rows, int32_t h_kv, int32_t d,
+                                 int32_t dtype, int32_t pos0, float rope_base,
+                                 const int32_t* planned, void* ws, size_t ws_bytes, void* stream) {
   msa_status s = check_heads(h_kv, d, dtype);
   if (s == MSA_OK) s = check_pool(page_size, n_pages, 1, 0);
   if (s != MSA_OK) return s;
@@ -148,10 +149,10 @@ msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32
           pos0);
   REQUIRE(ws != nullptr && ws_bytes >= kHeader && aligned(ws, 256), MSA_ERR_WORKSPACE,
           "workspace %zu bytes, need %zu (256-byte aligned)", ws_bytes, kHeader);
-  if (n_rows == 0) return done(cudaSuccess, "");
+  if (n_rows == 0 && planned == nullptr) return done(cudaSuccess, "");
   const int64_t row = (int64_t)h_kv * d, per16 = 16 / (int64_t)esize(dtype);
-  REQUIRE(slot_map && row_pos && K_new && V_new && K_pages && V_pages, MSA_ERR_INVALID_ARG,
-          "null tensor");
+  REQUIRE(n_rows == 0 || (slot_map && row_pos && K_new && V_new && K_pages && V_pages),
+          MSA_ERR_INVALID_ARG, "null tensor");
   REQUIRE(k_stride >= row && v_stride >= row && k_stride % per16 == 0 && v_stride % per16 == 0,
           MSA_ERR_INVALID_ARG, "row strides %lld, %lld (at least h_kv * d, multiples of 16 bytes)",
           (long long)k_stride, (long long)v_stride);
@@ -168,6 +169,7 @@ msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32
   p.V_pages = V_pages;
   p.n_slots = (int64_t)n_pages * page_size;
   p.n_rows = n_rows;
+  p.planned = planned;
   p.h_kv = h_kv;
   p.rope = rope_base > 0.f ? 1 : 0;
   p.pos0 = pos0;
@@ -175,6 +177,16 @@ msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32
   p.err = static_cast<int*>(ws);
   return done(msa::launch_paged_append(p, dtype, d, sm_count(), (cudaStream_t)stream),
               "msa_paged_append launch");
+}
+
+msa_status msa_paged_append(void* K_pages, void* V_pages, int32_t n_pages, int32_t page_size,
+                            const int32_t* slot_map, const int32_t* row_pos, const void* K_new,
+                            const void* V_new, int64_t k_stride, int64_t v_stride,
+                            int32_t n_rows, int32_t h_kv, int32_t d, int32_t dtype, int32_t pos0,
+                            float rope_base, void* ws, size_t ws_bytes, void* stream) {
+  return msa_paged_append_step(K_pages, V_pages, n_pages, page_size, slot_map, row_pos, K_new,
+                               V_new, k_stride, v_stride, n_rows, h_kv, d, dtype, pos0, rope_base,
+                               nullptr, ws, ws_bytes, stream);
 }
 
 size_t msa_paged_attend_workspace(int32_t n_rows, int32_t n_req, int32_t h_q, int32_t h_kv,

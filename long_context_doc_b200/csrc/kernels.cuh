@@ -386,6 +386,7 @@ struct PagedAppendParams {
   void* K_pages;           // [n_slots, h_kv, d]
   void* V_pages;
   int64_t n_slots;
+  const int32_t* planned;  // rows of the step (nullable: not checked against n_rows)
   int n_rows, h_kv, rope, pos0;
   unsigned long long rope_turns[64];
   int* err;

@@ -266,6 +266,8 @@ __global__ void __launch_bounds__(128, kAppendCtas) paged_append_kernel(PagedApp
   for (int e = 0; e < E; ++e) F[e] = p.rope_turns[c * E + e];
   const int nw = gridDim.x * (blockDim.x >> 5);
   wait_then_let_start();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.planned != nullptr && *p.planned > p.n_rows)
+    set_err(p.err, kErrBadIndex);  // rows have a place and are not given
   for (int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < p.n_rows; r += nw) {
     const int64_t slot = p.slot_map[r];
     if (slot < 0) continue;  // a padding row
@@ -328,8 +330,7 @@ cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st) 
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
                                 cudaStream_t st) {
-  if (p.n_rows == 0) return cudaSuccess;
-  const int grid = std::min((p.n_rows + 3) / 4, sms * pgd::kAppendCtas);
+  const int grid = std::max(1, std::min((p.n_rows + 3) / 4, sms * pgd::kAppendCtas));
   auto go = [&](auto kernel) { return launch_early(kernel, dim3(grid), dim3(128), 0, st, p); };
   if (dtype == 1)
     return d == 128 ? go(pgd::paged_append_kernel<__nv_bfloat16, 128>)

@@ -129,6 +129,19 @@ def test_cache_status_covers_attention(msa, gpu, T, dtype):
     assert cache.status() == 3
 
 
+@gpu_test
+@pytest.mark.parametrize("rows", [0, 1, 39])
+def test_cache_append_of_fewer_rows_than_planned(msa, gpu, rows):
+    """Rows that the plan has a place for and that append is not given are told of: attention
+    would read what their pages held before."""
+    cache, f = _two_request_step(msa, gpu, 20)
+    cache.append(0, f(rows, 2), f(rows, 2))
+    assert cache.status() == 3
+    cache.plan(_i32([50, 50], gpu))
+    cache.append(0, f(40, 2), f(40, 2))  # 20 planned rows, padded
+    assert cache.status() == 0
+
+
 def test_attend_step_refuses_a_misaligned_word(msa):
     ws = ctypes.c_void_p(512)
     f = ctypes.c_void_p(1024)
@@ -141,3 +154,12 @@ def test_attend_step_refuses_a_misaligned_word(msa):
     with pytest.raises(msa.MSAError, match="step_ws"):
         msa.paged_attend(torch.zeros(5, 4, 64), i32(3), i32(2), pool, pool, i32(2, 3), 0, 0.0,
                          step_ws=torch.zeros(8, dtype=torch.uint8))
+
+
+def test_append_refuses_a_bad_row_start(msa):
+    pool, i32 = torch.zeros(4, 16, 2, 64), lambda *s: torch.zeros(s, dtype=torch.int32)
+    new = torch.zeros(3, 2, 64)
+    for bad, text in ((torch.zeros(2, dtype=torch.int64), "row_start is torch.int64"),
+                      (i32(0), "row_start is empty"), (i32(4)[::2], "not contiguous")):
+        with pytest.raises(msa.MSAError, match=text):
+            msa.paged_append(pool, pool, i32(3), i32(3), new, new, 0, 0.0, row_start=bad)
