@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kFillThreads) page_fill_kernel(PagePlanParams 
 // 16-byte chunk of the lower half of a head and its partner half a head on (RoPE pairs
 // i, i + d/2), so a row's angles are computed once and serve every head. HBM-bound for many
 // rows (each row read and written once), latency for few.
-template <typename T, int D>
+template <typename T, int D, bool ROPE>
 __global__ void __launch_bounds__(128, kAppendCtas) paged_append_kernel(PagedAppendParams p) {
   constexpr int E = 16 / sizeof(T);   // elements of a chunk
   constexpr int HC = D / 2 / E;       // chunks of half a head
@@ -281,8 +281,10 @@ __global__ void __launch_bounds__(128, kAppendCtas) paged_append_kernel(PagedApp
     T* kd = static_cast<T*>(p.K_pages) + slot * p.h_kv * D;
     T* vd = static_cast<T*>(p.V_pages) + slot * p.h_kv * D;
     float2 cs[E];
+    if constexpr (ROPE) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) cs[e] = p.rope ? rot_turns(pos, F[e]) : make_float2(1.f, 0.f);
+      for (int e = 0; e < E; ++e) cs[e] = rot_turns(pos, F[e]);
+    }
 #pragma unroll 2
     for (int h = h0; h < p.h_kv; h += HPW) {
       const int at = h * D + c * E;
@@ -290,16 +292,18 @@ __global__ void __launch_bounds__(128, kAppendCtas) paged_append_kernel(PagedApp
       const Raw kb = __ldg(reinterpret_cast<const Raw*>(ks + at + D / 2));
       const Raw va = __ldg(reinterpret_cast<const Raw*>(vs + at));
       const Raw vb = __ldg(reinterpret_cast<const Raw*>(vs + at + D / 2));
-      float a[E], b[E];
-      V::unpack(ka, a);
-      V::unpack(kb, b);
-      Raw oa, ob;
-      T* ta = reinterpret_cast<T*>(&oa);
-      T* tb = reinterpret_cast<T*>(&ob);
+      Raw oa = ka, ob = kb;
+      if constexpr (ROPE) {  // (turned by angle 0, an infinity's partner would be NaN)
+        float a[E], b[E];
+        V::unpack(ka, a);
+        V::unpack(kb, b);
+        T* ta = reinterpret_cast<T*>(&oa);
+        T* tb = reinterpret_cast<T*>(&ob);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        ta[e] = Elem<T>::from_f(a[e] * cs[e].x - b[e] * cs[e].y);
-        tb[e] = Elem<T>::from_f(b[e] * cs[e].x + a[e] * cs[e].y);
+        for (int e = 0; e < E; ++e) {
+          ta[e] = Elem<T>::from_f(a[e] * cs[e].x - b[e] * cs[e].y);
+          tb[e] = Elem<T>::from_f(b[e] * cs[e].x + a[e] * cs[e].y);
+        }
       }
       *reinterpret_cast<Raw*>(kd + at) = oa;
       *reinterpret_cast<Raw*>(kd + at + D / 2) = ob;
@@ -331,12 +335,16 @@ cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st) 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
                                 cudaStream_t st) {
   const int grid = std::max(1, std::min((p.n_rows + 3) / 4, sms * pgd::kAppendCtas));
-  auto go = [&](auto kernel) { return launch_early(kernel, dim3(grid), dim3(128), 0, st, p); };
+  auto go = [&](auto plain, auto turned) {
+    return launch_early(p.rope ? turned : plain, dim3(grid), dim3(128), 0, st, p);
+  };
+  using pgd::paged_append_kernel;
+  using bf16 = __nv_bfloat16;
   if (dtype == 1)
-    return d == 128 ? go(pgd::paged_append_kernel<__nv_bfloat16, 128>)
-                    : go(pgd::paged_append_kernel<__nv_bfloat16, 64>);
-  return d == 128 ? go(pgd::paged_append_kernel<float, 128>)
-                  : go(pgd::paged_append_kernel<float, 64>);
+    return d == 128 ? go(paged_append_kernel<bf16, 128, false>, paged_append_kernel<bf16, 128, true>)
+                    : go(paged_append_kernel<bf16, 64, false>, paged_append_kernel<bf16, 64, true>);
+  return d == 128 ? go(paged_append_kernel<float, 128, false>, paged_append_kernel<float, 128, true>)
+                  : go(paged_append_kernel<float, 64, false>, paged_append_kernel<float, 64, true>);
 }
 
 }  // namespace msa

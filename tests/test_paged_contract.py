@@ -163,3 +163,24 @@ def test_append_refuses_a_bad_row_start(msa):
                       (i32(0), "row_start is empty"), (i32(4)[::2], "not contiguous")):
         with pytest.raises(msa.MSAError, match=text):
             msa.paged_append(pool, pool, i32(3), i32(3), new, new, 0, 0.0, row_start=bad)
+
+
+# ------------------------------------------------------------------ values
+@gpu_test
+@pytest.mark.parametrize("dtype,bits", [(torch.bfloat16, torch.int16), (torch.float32, torch.int32)],
+                         ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_without_rope_copies(msa, gpu, dtype, bits, d):
+    """Without RoPE the keys are stored as given, bit for bit: infinities, NaN, signed zeros."""
+    new = torch.randn(5, 3, d, device=gpu).to(dtype)
+    new[0, 0, 3] = float("inf")
+    new[1, 1, d // 2 + 7] = -float("inf")
+    new[2, 2, 1] = float("nan")
+    new[3] = -0.0
+    new[3, 0, d // 2:] = -2.0
+    K = torch.zeros(1, 16, 3, d, dtype=dtype, device=gpu)
+    V = torch.zeros_like(K)
+    msa.paged_append(K, V, _i32([4, 0, 9, 15, 2], gpu), _i32([0, 1, 2, 3, 4], gpu), new, new, 7,
+                     0.0)
+    for got in (K, V):
+        assert torch.equal(got[0, [4, 0, 9, 15, 2]].view(bits), new.view(bits))
