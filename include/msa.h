@@ -464,13 +464,13 @@ msa_status msa_encode_hidden(const void* H, int64_t n_tok, int32_t D, const void
  * counterpart). Row p of request r lies in page block_table[r, p / page_size] at row
  * p % page_size ("slot" = page * page_size + p % page_size); keys are stored rotated at
  * pos0 + p. A step is msa_page_plan once, then per layer msa_paged_append of the step's new
- * rows and msa_paged_attend of their queries (or their _step forms, which check more). New rows lie packed, request after request:
- * row_start[r] .. row_start[r + 1] are request r's. All lengths, counts and tables are int32 in
- * device memory, so a captured step replays with the current ones; rows behind the last
- * request's (padding) are neither read nor written.
+ * rows and msa_paged_attend of their queries (or their _step forms, which check more). New rows
+ * lie packed, request after request: row_start[r] .. row_start[r + 1] are request r's. All
+ * lengths, counts and tables are int32 in device memory, so a captured step replays with the
+ * current ones; rows behind the last request's (padding) are neither read nor written.
  * Limits: page_size a power of two from 16 to 2^20, n_req <= 4096, a pool of up to 2^31 - 1 and
- * a request of up to 2^30 rows, h_kv <= 1024. Requests may share pages that none of them appends
- * to.
+ * a request of up to 2^30 rows, h_kv <= 1024, h_q <= 2^20. Requests may share pages that none of
+ * them appends to.
  */
 
 /* msa_page_plan - block tables and slot maps of a step from the requests' lengths.

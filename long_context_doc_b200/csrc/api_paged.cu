@@ -36,6 +36,7 @@ msa_status done(cudaError_t e, const char* what) {
 
 constexpr size_t kHeader = 256;
 constexpr int32_t kMinPage = 16, kMaxHeads = 1024;
+constexpr int32_t kMaxQueryHeads = 1 << 20;  // offsets within a row of Q are 32-bit
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t esize(int dtype) { return dtype == MSA_BF16 ? 2 : 4; }
@@ -214,6 +215,7 @@ msa_status msa_paged_attend_step(const void* Q, int64_t q_stride, int32_t n_rows
   if (s != MSA_OK) return s;
   REQUIRE(h_q >= h_kv && h_q % h_kv == 0, MSA_ERR_INVALID_ARG, "h_q %d not a multiple of h_kv %d",
           h_q, h_kv);
+  REQUIRE(h_q <= kMaxQueryHeads, MSA_ERR_UNSUPPORTED, "h_q %d (up to %d)", h_q, kMaxQueryHeads);
   REQUIRE(n_rows >= 0 && (int64_t)n_rows * h_q < (1ll << 31) && max_ctx >= 0 && pos0 >= 0,
           MSA_ERR_INVALID_ARG, "bad sizes (n_rows=%d h_q=%d max_ctx=%d pos0=%d)", n_rows, h_q,
           max_ctx, pos0);

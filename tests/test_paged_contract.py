@@ -184,3 +184,16 @@ def test_append_without_rope_copies(msa, gpu, dtype, bits, d):
                      0.0)
     for got in (K, V):
         assert torch.equal(got[0, [4, 0, 9, 15, 2]].view(bits), new.view(bits))
+
+
+# ------------------------------------------------------------------ limits
+def test_attend_refuses_more_query_heads_than_it_indexes(msa):
+    """One row of 2^24 heads of 128 (4 GB of bf16) passes the kernels' 32-bit offsets in a row."""
+    f, ws = ctypes.c_void_p(1024), ctypes.c_void_p(512)
+    for h_q in ((1 << 20) + 1, 1 << 24, 1 << 25):
+        for d, dtype in ((64, 0), (128, 0), (128, 1)):
+            need = msa.msa_paged_attend_workspace(1, 1, h_q, 1, d, dtype, 0, 4, 16)
+            got = msa.lib.msa_paged_attend(f, h_q * d, 1, h_q, f, f, 1, f, f, 8, 16, f, 4, None,
+                                           None, None, 0, 1, d, dtype, 0, 0.0, 0.0, f, ws,
+                                           max(need, 256), None)
+            assert got == 2, (h_q, d, dtype)
