@@ -550,7 +550,11 @@ msa_status msa_paged_append_step(void* K_pages, void* V_pages, int32_t n_pages, 
  *            rotated query too, rounded to bf16. fp32: products of tf32 high
  *            and low parts (2^-22).
  * Rows of the request that a token does not see are given weight 0 exactly, but they are read
- * with the tile they share with visible ones: their V must be finite.
+ * with the tile they share with visible ones: their V must be finite. Of the rows it sees, a
+ * score of -inf has weight 0 (a token with no other gets 0), an infinite V makes its element
+ * infinite, and NaN and scores of +inf make the row NaN; but in blocks of 9 to 128 query rows per
+ * KV head (bf16, with the queries' low parts) an infinite key or query may make the row NaN in
+ * every case.
  * A request whose length, row starts or pages are out of range is recorded in the status word
  * (3); its rows of O are unspecified or not written, other requests' are right as long as no rows
  * are claimed twice. Status 1: a device wait expired; 2: more than 2^31 tiles of work (nothing

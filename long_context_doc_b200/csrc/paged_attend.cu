@@ -109,6 +109,15 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
 }
 
+// A sum of products with the operands' high parts plus those with the low parts. An infinite
+// operand has an infinite high part, whose products are what they should be, and a low part of
+// NaN, and the other operand's low part may have any sign or be 0: the low sum is left out where
+// it makes NaN of the high one.
+__device__ __forceinline__ float add_low(float hi, float lo) {
+  const float s = hi + lo;
+  return s == s ? s : hi;
+}
+
 template <int KT> __device__ __forceinline__ int ctx_tiles(const PagedReq& q) {
   return (q.C + KT - 1) / KT;
 }
@@ -531,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
           }
 #pragma unroll
           for (int n = 0; n < NK; ++n) {  // q_hi k + q_lo k
-            sc[n][0] += sc[n][2];
-            sc[n][1] += sc[n][3];
+            sc[n][0] = add_low(sc[n][0], sc[n][2]);
+            sc[n][1] = add_low(sc[n][1], sc[n][3]);
           }
         } else {
           // The tensor cores drop bits when they add to a running sum: the small products and
@@ -552,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            sc[0][e] = ((sh[0][e] + sh[1][e]) + (sh[2][e] + sh[3][e])) + sl[e];
+            sc[0][e] = add_low((sh[0][e] + sh[1][e]) + (sh[2][e] + sh[3][e]), sl[e]);
         }
         if (!full) {
 #pragma unroll
@@ -624,12 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             const uint32_t ch = 2 * nt + (gr >> 2), in = (gr & 3) * 4;
             split_tf32(lds32(vb + (2 * t4) * RB + ((ch ^ (2 * t4)) << 4) + in), h0, l0);
             split_tf32(lds32(vb + (2 * t4 + 1) * RB + ((ch ^ (2 * t4 + 1)) << 4) + in), h1, l1);
-            float d[4] = {0.f, 0.f, 0.f, 0.f};  // (added to the running sum in fp32)
-            mma_tf32(d, al, h0, h1);
-            mma_tf32(d, ah, l0, l1);
-            mma_tf32(d, ah, h0, h1);
+            // (added to the running sum in fp32)
+            float dl[4] = {0.f, 0.f, 0.f, 0.f}, dh[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_tf32(dl, al, h0, h1);
+            mma_tf32(dl, ah, l0, l1);
+            mma_tf32(dh, ah, h0, h1);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][e] += d[e];
+            for (int e = 0; e < 4; ++e) o[nt][e] += add_low(dh[e], dl[e]);
           }
         }
       }
@@ -638,8 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       if constexpr (BF) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {  // p_hi v + p_lo v
-          o[nt][0] += o[nt][2];
-          o[nt][1] += o[nt][3];
+          o[nt][0] = add_low(o[nt][0], o[nt][2]);
+          o[nt][1] = add_low(o[nt][1], o[nt][3]);
         }
       }
 #pragma unroll

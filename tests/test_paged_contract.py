@@ -186,6 +186,58 @@ def test_append_without_rope_copies(msa, gpu, dtype, bits, d):
         assert torch.equal(got[0, [4, 0, 9, 15, 2]].view(bits), new.view(bits))
 
 
+def _tolerance(dtype, rows, mag, n, spread, o, d):
+    """As in test_paged: of the low parts for up to eight rows per KV head, else of the type."""
+    if dtype == "bf16" and rows <= 8:
+        return (np.expm1(2 * 2.0 ** -15 * mag) + 2 * 2.0 ** -16) * spread + 2.0 ** -8 * np.abs(o)
+    u_s, u_p, u_o = ((2.0 ** -8 + 2.0 ** -20, 2.0 ** -8 + 2.0 ** -20, 2.0 ** -8) if dtype == "bf16"
+                     else ((3 + 3 * d / 8 + 4) * 2.0 ** -22, (4 + 3 * n / 8 + 8) * 2.0 ** -22,
+                           2.0 ** -23))
+    return (np.expm1(2 * u_s * mag) + 2 * u_p) * spread + u_o * np.abs(o)
+
+
+@gpu_test
+@pytest.mark.parametrize("dtype,T,what", [
+    *((dt, T, w) for dt, T in (("bf16", 1), ("bf16", 2), ("fp32", 1), ("fp32", 40), ("bf16", 40))
+      for w in "vkq"), ("bf16", 9, "v")])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_infinities(msa, gpu, dtype, T, d, what):
+    """Infinite elements that a token sees: one of V makes its dimension infinite; one of a key
+    makes its score infinite, so that it has weight 0 or makes the row NaN; one of the query does
+    so for every key."""
+    c = Case(gpu, 81, dtype, [300, 45], [T, T], 16, 8, 2, d, None, base=0.0)
+    inf = float("inf")
+    for r, i, j, sign in ((0, 3, 5, 1), (0, 200, d - 1, -1), (1, 2, 0, 1)):
+        if what != "q":
+            (c.K if what == "k" else c.V)[int(c.table[r, i // 16]), i % 16, :, j] = sign * inf
+            (c.k64 if what == "k" else c.v64)[r][i, :, j] = sign * inf
+    if what == "q":  # rows of request 1
+        c.Q[T:2 * T, :, 6] = -inf
+        c.q64[T:2 * T, :, 6] = -inf
+    O = c.run(msa)[:c.rows].double().cpu().numpy()
+    seen = {"nan": 0, "inf": 0, "finite": 0}
+    with np.errstate(invalid="ignore"):
+        for r in range(2):
+            for h in range(8):
+                k, v = c.k64[r][:, h // 4], c.v64[r][:, h // 4]
+                for t in range(T):
+                    n, q = c.lens[r] - T + t + 1, c.q64[r * T + t, h]
+                    s = k[:n] @ q * d ** -0.5
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    o = p @ v[:n]
+                    got, good = O[r * T + t, h], np.isfinite(o)
+                    np.testing.assert_array_equal(got[~good], o[~good])
+                    mag = np.abs(k[:n]) @ np.abs(q) * d ** -0.5
+                    mag = mag[np.isfinite(mag)].max(initial=0)
+                    tol = _tolerance(dtype, T * 4, mag, n, p @ np.abs(v[:n]), o, d)
+                    assert (np.abs(got - o) <= tol)[good].all(), (r, h, t)
+                    seen["nan"] += int(np.isnan(o).any())
+                    seen["inf"] += int(np.isinf(o).any())
+                    seen["finite"] += int(good.any())
+    assert seen["finite"] and (seen["inf"] if what == "v" else seen["nan"])
+
+
 # ------------------------------------------------------------------ limits
 def test_attend_refuses_more_query_heads_than_it_indexes(msa):
     """One row of 2^24 heads of 128 (4 GB of bf16) passes the kernels' 32-bit offsets in a row."""
