@@ -285,30 +285,40 @@ __global__ void __launch_bounds__(128, kAppendCtas) paged_append_kernel(PagedApp
 #pragma unroll
       for (int e = 0; e < E; ++e) cs[e] = rot_turns(pos, F[e]);
     }
-#pragma unroll 2
-    for (int h = h0; h < p.h_kv; h += HPW) {
-      const int at = h * D + c * E;
-      const Raw ka = __ldg(reinterpret_cast<const Raw*>(ks + at));
-      const Raw kb = __ldg(reinterpret_cast<const Raw*>(ks + at + D / 2));
-      const Raw va = __ldg(reinterpret_cast<const Raw*>(vs + at));
-      const Raw vb = __ldg(reinterpret_cast<const Raw*>(vs + at + D / 2));
-      Raw oa = ka, ob = kb;
-      if constexpr (ROPE) {  // (turned by angle 0, an infinity's partner would be NaN)
-        float a[E], b[E];
-        V::unpack(ka, a);
-        V::unpack(kb, b);
-        T* ta = reinterpret_cast<T*>(&oa);
-        T* tb = reinterpret_cast<T*>(&ob);
+    // two heads a turn, their loads in flight together
+    for (int hh = h0; hh < p.h_kv; hh += 2 * HPW) {
+      Raw ka[2], kb[2], va[2], vb[2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          ta[e] = Elem<T>::from_f(a[e] * cs[e].x - b[e] * cs[e].y);
-          tb[e] = Elem<T>::from_f(b[e] * cs[e].x + a[e] * cs[e].y);
-        }
+      for (int u = 0; u < 2; ++u) {
+        const int h = hh + u * HPW, at = h * D + c * E;
+        if (h >= p.h_kv) continue;
+        ka[u] = *reinterpret_cast<const Raw*>(ks + at);
+        kb[u] = *reinterpret_cast<const Raw*>(ks + at + D / 2);
+        va[u] = *reinterpret_cast<const Raw*>(vs + at);
+        vb[u] = *reinterpret_cast<const Raw*>(vs + at + D / 2);
       }
-      *reinterpret_cast<Raw*>(kd + at) = oa;
-      *reinterpret_cast<Raw*>(kd + at + D / 2) = ob;
-      *reinterpret_cast<Raw*>(vd + at) = va;
-      *reinterpret_cast<Raw*>(vd + at + D / 2) = vb;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = hh + u * HPW, at = h * D + c * E;
+        if (h >= p.h_kv) continue;
+        Raw oa = ka[u], ob = kb[u];
+        if constexpr (ROPE) {  // (turned by angle 0, an infinity's partner would be NaN)
+          float a[E], b[E];
+          V::unpack(ka[u], a);
+          V::unpack(kb[u], b);
+          T* ta = reinterpret_cast<T*>(&oa);
+          T* tb = reinterpret_cast<T*>(&ob);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            ta[e] = Elem<T>::from_f(a[e] * cs[e].x - b[e] * cs[e].y);
+            tb[e] = Elem<T>::from_f(b[e] * cs[e].x + a[e] * cs[e].y);
+          }
+        }
+        *reinterpret_cast<Raw*>(kd + at) = oa;
+        *reinterpret_cast<Raw*>(kd + at + D / 2) = ob;
+        *reinterpret_cast<Raw*>(vd + at) = va[u];
+        *reinterpret_cast<Raw*>(vd + at + D / 2) = vb[u];
+      }
     }
   }
 }

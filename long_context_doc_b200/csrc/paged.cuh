@@ -8,7 +8,9 @@
 
 namespace msa {
 
-// The kernels before this one in the stream are complete; the next one may be set up.
+// The kernels before this one in the stream are complete; the next one may be set up. Until then
+// this one may live beside kernels that write what it reads, so none of the paged kernels loads
+// through the non-coherent path (read-only data of the kernel's whole life).
 __device__ __forceinline__ void wait_then_let_start() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -24,10 +26,10 @@ struct PagedReq {
 __device__ __forceinline__ PagedReq paged_req(const PagedAttendParams& p, int r, int lo, int hi,
                                               int* bad) {
   PagedReq q;
-  q.a = __ldg(p.row_start + r);
-  q.T = __ldg(p.row_start + r + 1) - q.a;
-  q.L = __ldg(p.len + r);
-  q.C = p.ctx_len != nullptr ? min(max(__ldg(p.ctx_len + r), 0), p.max_ctx) : 0;
+  q.a = p.row_start[r];
+  q.T = p.row_start[r + 1] - q.a;
+  q.L = p.len[r];
+  q.C = p.ctx_len != nullptr ? min(max(p.ctx_len[r], 0), p.max_ctx) : 0;
   const bool ok = q.a >= 0 && q.T >= 0 && q.T <= p.n_rows - q.a && q.L >= 0 &&
                   q.L <= ((long long)p.max_pages << p.page_shift);
   if (!ok) *bad = kErrBadIndex;

@@ -157,13 +157,13 @@ __device__ __forceinline__ void rotate_queries(const PagedAttendParams& p, int w
 #pragma unroll
     for (int k = 0; k < NI; ++k) {  // (any row of Q may be read, whoever it belongs to)
       const int h = min(h0 + k * HPW, p.h_q - 1);
-      ra[k] = __ldg(reinterpret_cast<const uint4*>(src + h * D));
-      rb[k] = __ldg(reinterpret_cast<const uint4*>(src + h * D + D / 2));
+      ra[k] = *reinterpret_cast<const uint4*>(src + h * D);
+      rb[k] = *reinterpret_cast<const uint4*>(src + h * D + D / 2);
     }
     int lo = 0, hi = p.n_req;      // the request of token i: row_start[lo] <= i < row_start[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(p.row_start + mid) <= i) lo = mid;
+      if (p.row_start[mid] <= i) lo = mid;
       else hi = mid;
     }
     int ignore = 0;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       const int pg = ((c.t - c.CT) * KT) >> p.page_shift;
       if (!entered && pg - win >= 0 && pg - win < 31) return;
       win = pg;
-      window = __ldg(p.table + (int64_t)c.r * p.max_pages + min(pg + lane, p.max_pages - 1));
+      window = p.table[(int64_t)c.r * p.max_pages + min(pg + lane, p.max_pages - 1)];
     };
     look(ld, true);
     int looked = ld.r;  // request the window belongs to (-1: none yet)
@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         for (int kk = 0; kk < KS; ++kk)  // the values as stored; turned below
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            qh[kk][hf + 2 * e] = __ldg(reinterpret_cast<const uint32_t*>(
-                BF ? src + kk * 16 + e * 8 + 2 * t4 : src + kk * 8 + e * 4 + t4));
+            qh[kk][hf + 2 * e] = *reinterpret_cast<const uint32_t*>(
+                BF ? src + kk * 16 + e * 8 + 2 * t4 : src + kk * 8 + e * 4 + t4);
             if constexpr (BF) qh[kk][1 + 2 * e] = 0u;  // low parts
           }
       }

@@ -527,7 +527,7 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             const int k = k0 + piece * br;
             cur.load = piece < kN / br && k < w.q.L;
             if (cur.load) {
-              const int page = __ldg(p.table + (int64_t)w.r * p.max_pages + (k >> p.page_shift));
+              const int page = p.table[(int64_t)w.r * p.max_pages + (k >> p.page_shift)];
               if (page < 0 || page >= p.n_pages) {
                 err = kErrBadIndex;
                 cur.load = false;

@@ -1,5 +1,7 @@
 """What the paged local context promises beside its numbers: streams, errors, limits."""
 import ctypes
+import glob
+import os
 
 import numpy as np
 import pytest
@@ -249,3 +251,15 @@ def test_attend_refuses_more_query_heads_than_it_indexes(msa):
                                            None, None, 0, 1, d, dtype, 0, 0.0, 0.0, f, ws,
                                            max(need, 256), None)
             assert got == 2, (h_q, d, dtype)
+
+
+def test_kernels_that_start_early_use_ordinary_loads(msa):
+    """The paged kernels are launched while the one before them may still write their inputs. A
+    load through the non-coherent path is only defined for memory that nothing writes while the
+    kernel lives, and the compiler may move it ahead of the wait."""
+    files = glob.glob(os.path.join(os.path.dirname(msa.LIB_PATH), "csrc", "paged*.cu*"))
+    assert len(files) >= 4
+    for name in files:
+        with open(name) as f:
+            text = f.read()
+        assert "__ldg(" not in text and "global.nc" not in text, name
