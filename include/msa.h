@@ -467,10 +467,12 @@ msa_status msa_encode_hidden(const void* H, int64_t n_tok, int32_t D, const void
  * rows and msa_paged_attend of their queries (or their _step forms, which check more). New rows
  * lie packed, request after request: row_start[r] .. row_start[r + 1] are request r's. All
  * lengths, counts and tables are int32 in device memory, so a captured step replays with the
- * current ones; rows behind the last request's (padding) are neither read nor written.
+ * current ones; nothing depends on rows behind the last request's (padding), and their outputs are
+ * not written.
  * Limits: page_size a power of two from 16 to 2^20, n_req <= 4096, a pool of up to 2^31 - 1 and
  * a request of up to 2^30 rows, h_kv <= 1024, h_q <= 2^20. Requests may share pages that none of
- * them appends to.
+ * them appends to or gives back (the plan keeps no count of a page's holders: a shared page given
+ * back lies on the stack while the others still read it).
  */
 
 /* msa_page_plan - block tables and slot maps of a step from the requests' lengths.
@@ -534,7 +536,7 @@ msa_status msa_paged_append_step(void* K_pages, void* V_pages, int32_t n_pages, 
  *
  * Q          n_rows rows of [h_q, d], q_stride elements apart (a multiple of 16 bytes), before
  *            RoPE; row_start [n_req + 1] as written by msa_page_plan. Rows behind
- *            row_start[n_req] are neither read nor written in O.
+ *            row_start[n_req] may be read, to no effect, and are not written in O.
  * len        [n_req] local rows of each request, its T new ones included: token i is local row
  *            len - T + i, at position pos0 + that row. Local rows at or past len are never
  *            looked at (they may hold anything). A chunk longer than len has tokens before row
@@ -556,9 +558,10 @@ msa_status msa_paged_append_step(void* K_pages, void* V_pages, int32_t n_pages, 
  * KV head (bf16, with the queries' low parts) an infinite key or query may make the row NaN in
  * every case.
  * A request whose length, row starts or pages are out of range is recorded in the status word
- * (3); its rows of O are unspecified or not written, other requests' are right as long as no rows
- * are claimed twice. Status 1: a device wait expired; 2: more than 2^31 tiles of work (nothing
- * is computed).
+ * (3); its rows of O are unspecified or not written, other requests' are right as long as the row
+ * starts ascend. Status 1: a device wait expired; 2: the warp-level kernel's list (blocks of 8
+ * query rows per KV head, fp32 16, times 8 KB tiles of the request) has 2^31 tiles or more, and
+ * it computes nothing: one fp32 request of 262,144 new tokens at d = 128 with 4 heads a group.
  * ws         msa_paged_attend_workspace(...) bytes, 256-byte aligned, not shared with a call
  *            that runs at the same time. The result does not depend on its contents.
  * msa_paged_attend_step is the same call as a part of a step: a status that is not 0 is recorded

@@ -25,9 +25,11 @@ namespace pgd {
 // the stack at F .. F+R-P. No step depends on another's writes: entries read (below F; columns
 // below held(old)) are never entries written, so one pass over the rows fills the slots and the
 // table together. One CTA forms the sums and, for up to kPlanOneCta rows, fills the maps itself
-// (one launch; a token for each of 256 requests: 6.5 us); more rows are filled by a second
+// (one launch; a token for each of 256 requests: 6.1 us); more rows are filled by a second
 // launch that is set up meanwhile (a cluster that did both was held up by its sixteen SMs'
-// arithmetic: 14.6 us for 225,000 rows). Latency-bound.
+// arithmetic: 14.6 us for 225,000 rows). One launch and two: 256 requests with 1,024 new rows 4.2
+// and 6.1 us, 4,096 rows 5.2 and 6.4, 8,192 rows 7.2 and 7.3, 16,384 rows 11.2 and 7.0; 4,096
+// requests of one row 12.1 and 15.8. Latency-bound.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanOneCta = 4096;  // rows up to which a single CTA fills the maps
 constexpr int kFillThreads = 256;

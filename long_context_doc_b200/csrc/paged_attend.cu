@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
   }
   if (tid == 0) pre[p.n_req] = (int32_t)carry;
   __syncthreads();
-  // (2^31 tiles are hours of work: a list that long is refused rather than counted in 64 bits)
+  // (A list of 2^31 tiles is refused: its prefix sums are 32-bit, for as many of 64 bits do not
+  // fit beside the rings.)
   if (carry > INT_MAX) err = kErrCtxOverflow;
   const int64_t total = carry > INT_MAX ? 0 : carry;
   const int S = (int)max((int64_t)1, min((int64_t)S_max, total / G::MIN_TILES));
@@ -416,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
       const int nrow = min(kRows, (int)min((long long)kRows, (long long)cu.q.T * Gq - (long long)cu.blk * kRows));
       // The block's queries, rotated. A lane's fragment elements of dims i and i + D/2 are its
       // own, and the angles of a token are the same for all its heads: the warp computes them
-      // once into a table in shared memory, some tokens at a time (the first exactly, the next
-      // ones by rotating on: at most 15 steps of 2^-23).
+      // once into a table in shared memory, CAP tokens at a time (the first exactly, the next
+      // ones by rotating on: at most 3 steps of 2^-23 at d = 128, 7 at d = 64).
       int vis[HR], row_tok[HR];  // last local row that query rows gr (+ 8) see; their tokens
       const int tok0 = cu.blk * kRows / Gq;
       const int n_tok = (cu.blk * kRows + nrow - 1) / Gq - tok0 + 1;
@@ -1016,11 +1017,18 @@ PagedPlan paged_attend_plan(int n_rows, int n_req, int h_q, int h_kv, int d, int
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   // one CTA per SM; more when the heads alone need more warps
   pl.grid = std::max(sms, (h_kv + pga::kWarps - 1) / pga::kWarps);
-  pl.S = pl.grid * pga::kWarps / h_kv;
-  // The tcgen05 kernel serves the bf16 requests with more than 8 query rows per KV head. The
+  // (the merge lists the ranges of both kernels in shared memory: 1,332 on a B200)
+  pl.S = std::min(pl.grid * pga::kWarps / h_kv, pga::kMaxTails - sms);
+  // The tcgen05 kernel serves the bf16 requests with more than 8 query rows per KV head: 16
+  // requests of 8,000 rows (8 KV heads, d = 128) take 92 us on the warp-level kernel and 109 here
+  // with 8 query rows each, 165 and 110 with 9, 289 and 111 with 32 (64 of 1,000 rows at d = 64
+  // and 4 KV heads: 19 and 40 with 8, 27 and 40 with 12, 36 and 40 with 20). The
   // host sees only the totals: it leaves the launch out where no request can have so many, and
-  // where there is at most one new token per request on average (a decode step, where the launch
-  // would cost its latency and find nothing; the warp-level kernel serves a longer request too).
+  // where there is at most one new token per slot of the table (a decode step, where the launch
+  // finds nothing and costs 4 to 5 us: the 64 requests with 8 rows each, 19.4 -> 24.7 us). What
+  // that costs: a chunk in a step of no more rows than slots stays on the warp-level kernel, which
+  // passes over the keys for every 8 rows (one request over 32,768 rows in a table of 256 slots:
+  // 4 tokens 41 us against 51, 16 tokens 118 against 53, 200 tokens 1,260 against 157).
   const int Gq = h_q / h_kv;
   const bool tc = dtype == 1 && Gq <= 256 && (int64_t)n_rows * Gq > kPagedWarpRows &&
                   (n_rows > n_req || Gq > kPagedWarpRows);

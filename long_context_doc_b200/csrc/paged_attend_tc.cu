@@ -23,7 +23,8 @@
 // 1.7 times that of the output's own rounding; one half: 1.4 times). The probabilities' low parts
 // would add 27% to a long chunk's time, the queries' need 64 KB that two halves do not have.
 // Bound by the chain scores -> softmax -> product: tensor pipe and exponentials are each busy half
-// of the time (2,048 tokens over 32,768 rows: 0.98 ms, 1.09 PFLOP/s).
+// of the time (2,048 tokens over 32,768 rows: 0.95-0.99 ms, 1.08-1.13 PFLOP/s, and 1.09-1.12 ms,
+// 0.95-0.98 PFLOP/s, where replays back to back meet the power cap).
 // Every wait is bounded; on expiry the CTA records kErrWaitTimeout, lets its copies and MMAs
 // land, frees its TMEM and leaves the rest unwritten.
 #include <cuda.h>
@@ -433,7 +434,6 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
       // one page (or memory tile) and 64 dims a lane
       Work w;
       walk.first_of(w, start_r, start_off, x0);
-      if (w.t0 == w.t1 && w.more) walk.next(w, lane);
       uint32_t seq = 0;
       const int ps = 1 << p.page_shift;
       const int br = min(ps, kN);               // rows of a box
