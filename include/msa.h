@@ -69,7 +69,8 @@ int msa_version(void);
 
 /* msa_set_device_wait_limit - the limit, in SM clock cycles, after which the consumer-side
  * waits of the tensor-core routing scan (its epilogue warps waiting for the tensor cores'
- * accumulators) give up: the kernel then records MSA_ERR_DEVICE's code 1 in the workspace
+ * accumulators) and of the paged attention's tcgen05 kernel (its softmax warps waiting for the
+ * scores) give up: the kernel then records MSA_ERR_DEVICE's code 1 in the workspace
  * status word, stops issuing, lets the copies and MMAs it issued land, frees its tensor memory
  * and returns (outputs undefined). Copies and MMAs in flight are always waited for with the
  * default limit. cycles <= 0 restores the default (2^31 cycles, about a second). Process-wide,

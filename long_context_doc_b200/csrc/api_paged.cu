@@ -286,6 +286,7 @@ msa_status msa_paged_attend_step(const void* Q, int64_t q_stride, int32_t n_rows
   p.q_rot = reinterpret_cast<__nv_bfloat16*>(take(pl.q_bytes));
   p.tc_rows = pl.tc_grid > 0 ? msa::kPagedWarpRows : INT32_MAX;
   p.tc_err_at = pl.grid;
+  p.wait_limit = msa::device_wait_limit();
   return done(msa::launch_paged_attend(p, pl, dtype, d, st), "msa_paged_attend launch");
 }
 

@@ -422,6 +422,7 @@ struct PagedAttendParams {
   float* part_o;            // [S][2][h_kv][8 or 16][d]
   int tc_rows;              // requests with more query rows per KV head take the tcgen05 kernel
   int tc_err_at;            // its first entry of err_cta
+  long long wait_limit;     // its softmax warps' waits for scores, SM clocks (0: default)
   int4* tc_tail;            // [tc_grid][2]
   float* tc_ml;             // [tc_grid][2][256][2] its partials
   float* tc_o;              // [tc_grid][2][256][d]

@@ -25,8 +25,9 @@
 // Bound by the chain scores -> softmax -> product: tensor pipe and exponentials are each busy half
 // of the time (2,048 tokens over 32,768 rows: 0.95-0.99 ms, 1.08-1.13 PFLOP/s, and 1.09-1.12 ms,
 // 0.95-0.98 PFLOP/s, where replays back to back meet the power cap).
-// Every wait is bounded; on expiry the CTA records kErrWaitTimeout, lets its copies and MMAs
-// land, frees its TMEM and leaves the rest unwritten.
+// Every wait is bounded (the softmax warps' for scores by the limit that
+// msa_set_device_wait_limit sets); on expiry the CTA records kErrWaitTimeout, lets its copies and
+// MMAs land, frees its TMEM and leaves the rest unwritten.
 #include <cuda.h>
 
 #include <algorithm>
@@ -173,6 +174,23 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t par, int* 
   while (!mbar_try_wait(bar, par)) {
     if (*abort_flag) return false;
     if (clock64() - t0 > kDefaultWaitLimit) {
+      set_err(err, kErrWaitTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same with the limit of the call, which msa_set_device_wait_limit sets: polling, so that the
+// limit and not the hardware's suspend time decides.
+__device__ __forceinline__ bool poll_or_abort(uint64_t* bar, uint32_t par, long long limit, int* err,
+                                              volatile int* abort_flag) {
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_test_wait(bar, par)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
       set_err(err, kErrWaitTimeout);
       *abort_flag = 1;
       return false;
@@ -719,7 +737,11 @@ paged_attend_tc_kernel(const __grid_constant__ CUtensorMap map_k,
             const bool alt = !two && ((t - t0) & 1);   // the second scores buffer
             const int bar = alt ? 2 : h;
             const uint32_t s_col = lane_base + (alt ? 128 : h * 128);
-            ok = wait(&sfull[bar], (alt ? n_alt++ : n_own++) & 1);
+            const uint32_t par = (alt ? n_alt++ : n_own++) & 1;
+            ok = p.wait_limit == 0
+                     ? wait(&sfull[bar], par)
+                     : __all_sync(0xffffffffu, poll_or_abort(&sfull[bar], par, p.wait_limit,
+                                                             &cta_err, abort_flag));
             if (!ok) break;
             fence_after();
             // V rows past the end hold anything: cleared, for 0 * NaN would reach O

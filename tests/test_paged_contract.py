@@ -144,6 +144,25 @@ def test_cache_append_of_fewer_rows_than_planned(msa, gpu, rows):
     assert cache.status() == 0
 
 
+@gpu_test
+@pytest.mark.parametrize("T,d", [(40, 128), (5, 128), (40, 64)])
+def test_attend_wait_timeout_is_reported_and_the_stream_recovers(msa, gpu, T, d):
+    """A limit of a few dozen cycles, which no scores meet: the wait runs out, the status says so,
+    copies and MMAs land, and the next call is right."""
+    c = Case(gpu, 91, "bf16", [900, 250, 40], [T] * 3, 32, 16, 4, d, [9, 0, 3])
+    ws, O = c.workspace(msa), torch.zeros(c.total, 16, d, dtype=c.tt, device=gpu)
+    step_ws = torch.zeros(256, dtype=torch.uint8, device=gpu)
+    prev = msa.msa_set_device_wait_limit(64)
+    try:
+        c.run(msa, O=O, ws=ws, step_ws=step_ws)
+        code = msa.msa_workspace_status(ws)  # synchronises the stream
+    finally:
+        assert msa.msa_set_device_wait_limit(prev) == 64
+    assert code == 1 and msa.msa_workspace_status(step_ws) == 1
+    c.check(c.run(msa, O=O, ws=ws))
+    assert msa.msa_workspace_status(ws) == 0
+
+
 def test_attend_step_refuses_a_misaligned_word(msa):
     ws = ctypes.c_void_p(512)
     f = ctypes.c_void_p(1024)
