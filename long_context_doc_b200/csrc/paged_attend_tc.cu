@@ -20,8 +20,10 @@
 // itself: the scores of a tile are formed before the product of the tile before it, and with the
 // queries' low parts too (their place in shared memory is the other half's).
 // Roundings: the probabilities to bf16 once, the queries of two halves as well (the mean error is
-// 1.7 times that of the output's own rounding; one half: 1.4 times). The probabilities' low parts
-// would add 27% to a long chunk's time, the queries' need 64 KB that two halves do not have.
+// 1.7 times that of the output's own rounding; one half: 1.4 times). For a chunk of 2,048 tokens
+// over 32,768 rows the probabilities' low parts add 27%, the queries' of two halves 22% (a ring of
+// three tiles instead of four, no staging of the output, half as many products again: 1.20 ms for
+// 0.98, 1.33-1.51 for 1.09 at the power cap; 24 mixed requests 460-490 us for 380-420).
 // Bound by the chain scores -> softmax -> product: tensor pipe and exponentials are each busy half
 // of the time (2,048 tokens over 32,768 rows: 0.95-0.99 ms, 1.08-1.13 PFLOP/s, and 1.09-1.12 ms,
 // 0.95-0.98 PFLOP/s, where replays back to back meet the power cap).

@@ -259,6 +259,18 @@ def test_attend_infinities(msa, gpu, dtype, T, d, what):
     assert seen["finite"] and (seen["inf"] if what == "v" else seen["nan"])
 
 
+@gpu_test
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_into_rows_aligned_to_16_bytes(msa, gpu, d):
+    c = Case(gpu, 33, "bf16", [300, 700, 45], [40, 5, 45], 16, 8, 2, d, [4, 0, 9])
+    n = c.total * 8 * d
+    buf = torch.full((n + 16,), 7.0, dtype=c.tt, device=gpu)
+    O = buf[8:8 + n].view(c.total, 8, d)
+    assert O.data_ptr() % 32 == 16
+    c.check(c.run(msa, O=O))
+    assert (O[c.rows:] == 7.0).all() and (buf[:8] == 7.0).all() and (buf[8 + n:] == 7.0).all()
+
+
 # ------------------------------------------------------------------ limits
 def test_attend_refuses_more_query_heads_than_it_indexes(msa):
     """One row of 2^24 heads of 128 (4 GB of bf16) passes the kernels' 32-bit offsets in a row."""
