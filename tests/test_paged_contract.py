@@ -294,3 +294,31 @@ def test_kernels_that_start_early_use_ordinary_loads(msa):
         with open(name) as f:
             text = f.read()
         assert "__ldg(" not in text and "global.nc" not in text, name
+
+
+@gpu_test
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attend_at_the_most_kv_heads(msa, gpu, dtype):
+    c = Case(gpu, 44, dtype, [50, 3], [1, 1], 16, 1024, 1024, 64, [2, 0])
+    c.check(c.run(msa))
+
+
+@gpu_test
+def test_a_cache_without_requests_and_calls_without_rows(msa, gpu):
+    cache = msa.PagedCache(0, 4, 16, 1, 8, 2, 64, device=gpu)
+    f = lambda n, h: torch.randn(n, h, 64, device=gpu).bfloat16()
+    plan = cache.plan(torch.zeros(0, dtype=torch.int32, device=gpu))
+    cache.append(0, f(8, 2), f(8, 2))
+    O = torch.full((8, 8, 64), 5.0, dtype=torch.bfloat16, device=gpu)
+    cache.attend(0, f(8, 8), O=O)
+    assert cache.status() == 0 and (O == 5.0).all()
+    assert plan["row_start"].tolist() == [0] and plan["slot_map"].tolist() == [-1] * 8
+    cache = msa.PagedCache(2, 4, 16, 1, 8, 2, 64, device=gpu)
+    cache.plan(_i32([0, 0], gpu))
+    cache.append(0, f(0, 2), f(0, 2))
+    assert cache.attend(0, f(0, 8)).shape == (0, 8, 64)
+    assert cache.status() == 0
+    cache.plan(_i32([2, 1], gpu))
+    cache.append(0, f(3, 2), f(3, 2))
+    assert cache.attend(0, f(3, 8)).isfinite().all()
+    assert cache.status() == 0

@@ -121,6 +121,12 @@ KEYS = {
     "mixed": ([700, 33, 400, 1, 2129], [1, 33, 100, 1, 60], 128, 16, 4, 128, [8, 0, 40, 3, 1]),
     "big_page": ([3000, 300], [100, 300], 1024, 8, 2, 128, None),
     "chunk_longer_than_context": ([100, 0], [300, 40], 16, 8, 2, 128, [9, 0]),
+    "256_heads_each": ([400, 70], [3, 1], 16, 256, 1, 128, [5, 0]),
+    "129_heads_each": ([400, 70], [3, 1], 16, 258, 2, 64, [0, 130]),
+    "85_heads_each": ([400, 700], [7, 30], 32, 85, 1, 128, [5, 0]),
+    "1024_kv_heads": ([200, 33], [12, 9], 16, 1024, 1024, 64, [3, 0]),
+    "one_token_of_17_heads": ([3000, 129, 1], [1, 1, 1], 16, 34, 2, 128, [64, 0, 0]),
+    "long": ([70000], [5], 64, 8, 1, 128, [128]),
     "a_key_past_a_tile": ([129, 257, 128, 256], [3, 65, 3, 65], 16, 16, 4, 128, [129, 128, 0, 1]),
 }
 
