@@ -705,6 +705,8 @@ def _explain_pool(what: str, K_pages, V_pages):
 
 def _raw_stream(dev: int, stream) -> int:
     """Handle of ``stream``, or of the current one of device ``dev``."""
+    if dev < 0:
+        raise MSAError(1, "the tensors are not in device memory")
     if stream is None:
         # the raw handle of torch.cuda.current_stream(dev), at a twentieth of its 3 us
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -726,8 +728,6 @@ def _made_on(dev: int, stream):
 
 def _launch(dev: int, stream, f, *args):
     """f(*args, stream) with device ``dev`` current, on ``stream`` or the device's current one."""
-    if dev < 0:
-        raise MSAError(1, "the tensors are not in device memory")
     stream = _raw_stream(dev, stream)
     if torch.cuda.current_device() == dev:
         status = f(*args, stream)

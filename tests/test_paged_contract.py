@@ -322,3 +322,14 @@ def test_a_cache_without_requests_and_calls_without_rows(msa, gpu):
     cache.append(0, f(3, 2), f(3, 2))
     assert cache.attend(0, f(3, 8)).isfinite().all()
     assert cache.status() == 0
+
+
+@pytest.mark.parametrize("stream", [None, 0, 1234])
+def test_a_cache_on_the_host_is_refused(msa, stream):
+    cache = msa.PagedCache(1, 4, 16, 2, 8, 2, 64, device="cpu")
+    rows = lambda h: torch.zeros(2, h, 64, dtype=torch.bfloat16)
+    for call in (lambda: cache.plan(torch.ones(1, dtype=torch.int32), stream=stream),
+                 lambda: cache.append(0, rows(2), rows(2), stream=stream),
+                 lambda: cache.attend(0, rows(4), stream=stream)):
+        with pytest.raises(msa.MSAError, match="device memory"):
+            call()
