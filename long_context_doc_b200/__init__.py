@@ -12,7 +12,6 @@ The lower-case helpers (``encode_pool``, ``route_topk``, ``gather``, ``sparse_at
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -713,17 +712,22 @@ def _raw_stream(dev: int, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _made_on(dev: int, stream):
-    """Context in which a call makes the tensors that it was not given: its own stream's. What
-    fills them comes before the call's kernels there, and their memory is not handed on to other
-    work of the current stream while these run."""
+def _made_on(dev: int, stream, make, *args):
+    """make(*args), the tensors that a call was not given, on the call's own stream: what fills
+    them comes before its kernels there, and their memory is not handed on to other work of the
+    current stream while these run."""
     if stream is None or dev < 0:
-        return contextlib.nullcontext()
+        return make(*args)
     if not isinstance(stream, torch.cuda.Stream):
         handle = _raw_stream(dev, stream)
         stream = (torch.cuda.ExternalStream(handle, device=dev) if handle else
                   torch.cuda.default_stream(dev))
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
+def _zeroed_ws(device) -> torch.Tensor:
+    return torch.zeros(256, dtype=torch.uint8, device=device)
 
 
 def _launch(dev: int, stream, f, *args):
@@ -753,11 +757,11 @@ def page_plan(target, length, n_free, block_table, free_list, page_size: int, ma
     n_free, row_start, slot_map, row_pos). ``out`` gives these tensors (its length and n_free
     may be the arguments themselves); device-side errors are in the status word of ``ws``."""
     n_req, dev = block_table.shape[0], block_table.get_device()
-    with _made_on(dev, stream):
-        if out is None:
-            out = page_plan_buffers(n_req, max_rows, block_table.device)
-        if ws is None:
-            ws = _ws(msa_page_plan_workspace(n_req, max_rows), block_table.device)
+    if out is None:
+        out = _made_on(dev, stream, page_plan_buffers, n_req, max_rows, block_table.device)
+    if ws is None:
+        ws = _made_on(dev, stream, _ws, msa_page_plan_workspace(n_req, max_rows),
+                      block_table.device)
     wanted = ((target, n_req), (length, n_req), (n_free, 1), (free_list, free_list.numel()),
               (block_table, block_table.numel()), (out["length"], n_req), (out["n_free"], 1),
               (out["row_start"], n_req + 1), (out["slot_map"], max_rows),
@@ -787,8 +791,7 @@ def paged_append(K_pages, V_pages, slot_map, row_pos, K_new, V_new, pos0: int, r
     that it has a place for: fewer set the status word too."""
     dt, dev, i32 = K_pages.dtype, K_pages.get_device(), torch.int32
     if ws is None:
-        with _made_on(dev, stream):
-            ws = torch.zeros(256, dtype=torch.uint8, device=K_pages.device)
+        ws = _made_on(dev, stream, _zeroed_ws, K_pages.device)
     n_rows, h_kv, d = K_new.shape
     if not (K_pages.dim() == 4 and K_pages.shape == V_pages.shape and
             K_pages.shape[2:] == K_new.shape[1:] and K_new.shape == V_new.shape and
@@ -838,8 +841,7 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
     n_req, max_pages = block_table.shape
     max_ctx = 0 if ctxK is None else ctxK.shape[1]
     if O is None:
-        with _made_on(dev, stream):
-            O = torch.empty((n_rows, h_q, d), dtype=dt, device=K_pages.device)
+        O = _made_on(dev, stream, K_pages.new_empty, (n_rows, h_q, d))
     if not (K_pages.shape == V_pages.shape and K_pages.shape[3] == d and O.shape == Q.shape and
             V_pages.dtype == dt and Q.dtype == dt and O.dtype == dt and
             row_start.dtype == i32 and length.dtype == i32 and block_table.dtype == i32 and
@@ -870,14 +872,14 @@ def paged_attend(Q, row_start, length, K_pages, V_pages, block_table, pos0: int,
                         ctxK=(ctxK, dt, None), ctxV=(ctxV, dt, None),
                         ctx_len=(ctx_len, i32, n_req))
     if ws is None:
-        with _made_on(dev, stream):
-            ws = _ws(msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q),
-                                                max_ctx, max_pages, page), Q.device)
+        ws = _made_on(dev, stream, _ws,
+                      msa_paged_attend_workspace(n_rows, n_req, h_q, h_kv, d, dtype_code(Q),
+                                                 max_ctx, max_pages, page), Q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         _explain_arrays("paged_attend", dev, ws=(ws, None, None))
-    if step_ws is not None:
-        _need("paged_attend", step_ws.get_device() == dev and step_ws.is_contiguous() and
-              step_ws.nbytes >= 256, "step_ws is not a workspace on the tensors' device")
+    if step_ws is not None and not (step_ws.get_device() == dev and step_ws.is_contiguous() and
+                                    step_ws.nbytes >= 256):
+        raise MSAError(1, "paged_attend: step_ws is not a workspace on the tensors' device")
     if ctxK is None:
         mem = (None, None, None)
     else:
@@ -946,8 +948,7 @@ class PagedCache:
                                               0 if ctxK is None else ctxK.shape[1], max_pages,
                                               self.page_size)
             if not kept or kept[-1].numel() < need:
-                with _made_on(dev, stream):
-                    kept.append(_ws(need, self.K.device))
+                kept.append(_made_on(dev, stream, _ws, need, self.K.device))
             ws = kept[-1]
         return paged_attend(Q, self.out["row_start"], self.length, self.K[layer], self.V[layer],
                             self.block_table, self.pos0, self.rope_base, ctxK, ctxV, ctx_len,
