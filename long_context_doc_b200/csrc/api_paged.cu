@@ -168,15 +168,15 @@ msa_status msa_paged_append_step(void* K_pages, void* V_pages, int32_t n_pages, 
   p.row_pos = row_pos;
   p.K_pages = K_pages;
   p.V_pages = V_pages;
-  p.n_slots = (int64_t)n_pages * page_size;
+  p.n_slots = n_pages * page_size;  // below 2^31
   p.n_rows = n_rows;
   p.planned = planned;
   p.h_kv = h_kv;
-  p.rope = rope_base > 0.f ? 1 : 0;
   p.pos0 = pos0;
-  if (p.rope) rope_fractions((double)rope_base, d, p.rope_turns);
+  const bool rope = rope_base > 0.f;
+  if (rope) rope_fractions((double)rope_base, d, p.rope_turns);
   p.err = static_cast<int*>(ws);
-  return done(msa::launch_paged_append(p, dtype, d, sm_count(), (cudaStream_t)stream),
+  return done(msa::launch_paged_append(p, rope, dtype, d, sm_count(), (cudaStream_t)stream),
               "msa_paged_append launch");
 }
 

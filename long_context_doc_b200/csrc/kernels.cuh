@@ -385,13 +385,12 @@ struct PagedAppendParams {
   const int32_t* row_pos;  // [n_rows]
   void* K_pages;           // [n_slots, h_kv, d]
   void* V_pages;
-  int64_t n_slots;
   const int32_t* planned;  // rows of the step (nullable: not checked against n_rows)
-  int n_rows, h_kv, rope, pos0;
+  int n_slots, n_rows, h_kv, pos0;
   unsigned long long rope_turns[64];
   int* err;
 };
-cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
+cudaError_t launch_paged_append(const PagedAppendParams& p, bool rope, int dtype, int d, int sms,
                                 cudaStream_t st);
 
 // ---- paged_attend.cu: attention of ragged requests over [routed memory ; paged local context]

@@ -344,11 +344,11 @@ cudaError_t launch_page_plan(const PagePlanParams& p, int sms, cudaStream_t st) 
   return launch_early(pgd::page_fill_kernel, dim3(grid), dim3(pgd::kFillThreads), 0, st, p);
 }
 
-cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int d, int sms,
+cudaError_t launch_paged_append(const PagedAppendParams& p, bool rope, int dtype, int d, int sms,
                                 cudaStream_t st) {
   const int grid = std::max(1, std::min((p.n_rows + 3) / 4, sms * pgd::kAppendCtas));
   auto go = [&](auto plain, auto turned) {
-    return launch_early(p.rope ? turned : plain, dim3(grid), dim3(128), 0, st, p);
+    return launch_early(rope ? turned : plain, dim3(grid), dim3(128), 0, st, p);
   };
   using pgd::paged_append_kernel;
   using bf16 = __nv_bfloat16;
